@@ -29,6 +29,9 @@ __all__ = [
     "Fv5Matrix", "tern_fv5_packed_bytes", "tern_fv5_pack", "tern_fv5_gemm", "tern_fv5_gemv_batch",
     "fv5b_head_gemv_argmax",
     "tern_rans_payload_bound", "tern_rans_workspace_bytes", "tern_rans_encode", "tern_rans_decode",
+    "TERN_ELEM_F32", "TERN_ELEM_BF16", "TERN_KV_BLOCK",
+    "QkvSpec", "KvCache", "KvBatch", "tern_rope_freqs", "tern_qk_norm_rope", "tern_kv_append", "tern_kv_read",
+    "tern_paged_attn_workspace_bytes", "tern_paged_attn",
     "TERN_PRO_NONE", "TERN_PRO_BF16", "TERN_PRO_CAST", "TERN_PRO_RMSNORM", "TERN_PRO_SWIGLU",
     "tern_status_string",
 ]
@@ -40,6 +43,8 @@ TERN_FLAG_PDL = 1
 TERN_FLAG_TCGEN05 = 2
 TERN_HEAD_NOALLOC_MAX_M = 16
 TERN_PRO_NONE, TERN_PRO_BF16, TERN_PRO_CAST, TERN_PRO_RMSNORM, TERN_PRO_SWIGLU = range(5)
+TERN_ELEM_F32, TERN_ELEM_BF16 = 0, 1
+TERN_KV_BLOCK = 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libterngemv.so")
@@ -106,6 +111,11 @@ def lib() -> ctypes.CDLL:
             "tern_rans_workspace_bytes": ([i32, i32], sz),
             "tern_rans_encode": ([vp, i32, i32, vp, vp, vp, sz, vp, sz, vp, vp], i32),
             "tern_rans_decode": ([vp, i32, vp, vp], i32),
+            "tern_qk_norm_rope": ([vp, i32, vp, vp, vp, u32, vp], i32),
+            "tern_kv_append": ([vp, vp, vp, vp, vp, u32, vp], i32),
+            "tern_kv_read": ([vp, vp, vp, vp, vp, vp], i32),
+            "tern_paged_attn_workspace_bytes": ([i32, i32, i32], sz),
+            "tern_paged_attn": ([vp, i32, ctypes.c_float, vp, vp, i32, vp, vp, vp, sz, vp, u32, vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -482,3 +492,209 @@ class GemvBatch:
             return
         _check(lib().tern_gemm_batch(self._arr, len(self.entries), self.M, self.act, _ptr(self.workspace),
                                      int(self.workspace.numel()), flags, _stream(stream)), "tern_gemm_batch")
+
+
+# ---- between the q|k|v linear and the o linear (include/tern.h: paged 8-bit cache, attention) ----
+
+class _Qkv(ctypes.Structure):
+    _fields_ = [("src_dev", ctypes.c_void_p), ("src_type", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("row_stride", ctypes.c_int64),
+                ("q_gain_dev", ctypes.c_void_p), ("k_gain_dev", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("freq_dev", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+                ("k_scale_dev", ctypes.c_void_p), ("v_scale_dev", ctypes.c_void_p)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("row_start_dev", ctypes.c_void_p), ("kv_len_dev", ctypes.c_void_p),
+                ("page_table_dev", ctypes.c_void_p)]
+
+
+def _want(t, what: str, dtypes, shape=None, device=None):
+    """A tensor argument of the calls below: type, shape (None: any extent), contiguity and device.
+    `device` is the first tensor's; that one must be on the current CUDA device, where the kernels run."""
+    import torch
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: not contiguous")
+    if not t.is_cuda or t.device != (device if device is not None else torch.device("cuda", torch.cuda.current_device())):
+        raise ValueError(f"{what}: on {t.device}, not on the device of the call")
+    return t
+
+
+def tern_rope_freqs(head_dim: int, base: float = 1e6, device="cuda"):
+    """fp64 [head_dim / 2] radians per position of the plain rotation: base^(-2i / head_dim)."""
+    import torch
+    return float(base) ** (-torch.arange(0, head_dim, 2, dtype=torch.float64, device=device) / head_dim)
+
+
+class QkvSpec:
+    """How q|k|v rows become queries and keys (tern_qkv in include/tern.h): head counts, head_dim 64 or
+    128, fp64 rotation frequencies [head_dim / 2], bf16 gains [head_dim] or None (no norm), eps."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, freq, q_gain=None, k_gain=None, eps: float = 1e-6):
+        import torch
+        self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        self.freq, self.q_gain, self.k_gain = freq, q_gain, k_gain
+        _want(freq, "freq", (torch.float64,), (self.head_dim // 2,))
+        self.device = freq.device
+        for g, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+            if g is not None:
+                _want(g, what, (torch.bfloat16,), (self.head_dim,), self.device)
+        self._c = _Qkv(None, TERN_ELEM_F32, self.q_heads, self.kv_heads, self.head_dim, 0, _ptr(q_gain), _ptr(k_gain),
+                       float(eps), _ptr(freq))
+        self._types = {torch.float32: TERN_ELEM_F32, torch.bfloat16: TERN_ELEM_BF16}
+
+    def _at(self, src, heads_per_kv: int):
+        """The descriptor of rows src [rows, width] (any row stride the library takes)."""
+        kind = self._types.get(src.dtype)
+        if kind is None:
+            raise ValueError(f"src: dtype {src.dtype}, expected torch.float32 or torch.bfloat16")
+        if src.dim() != 2 or src.shape[1] < (self.q_heads + heads_per_kv * self.kv_heads) * self.head_dim or \
+                src.stride(1) != 1 or src.device != self.device:
+            raise ValueError("src: expected rows [rows, >= heads * head_dim] with unit column stride on the spec's device")
+        c = _Qkv.from_buffer_copy(self._c)
+        c.src_dev, c.src_type = src.data_ptr(), kind
+        c.row_stride = src.stride(0) if src.shape[0] > 1 else max(src.stride(0), src.shape[1] + -src.shape[1] % 4)
+        return c
+
+
+class KvCache:
+    """A paged int8 key/value cache: codes int8 [pages, kv_heads, page_size, head_dim] and fp32 scales
+    [pages, kv_heads, page_size / 16] for keys and for values."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4 or k.shape[2] % TERN_KV_BLOCK:
+            raise ValueError("k: expected int8 [pages, kv_heads, page_size, head_dim] with page_size a multiple of 16")
+        self.pages, self.kv_heads, self.page_size, self.head_dim = (int(n) for n in k.shape)
+        _want(k, "k", (torch.int8,))
+        self.device = k.device
+        _want(v, "v", (torch.int8,), k.shape, self.device)
+        for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _want(s, what, (torch.float32,), (self.pages, self.kv_heads, self.page_size // TERN_KV_BLOCK), self.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = _KvCache(self.pages, self.page_size, self.kv_heads, self.head_dim, _ptr(k), _ptr(v), _ptr(k_scale),
+                           _ptr(v_scale))
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def empty(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        """A cache without tokens (its memory needs no initialisation)."""
+        import torch
+        codes = [torch.empty(pages, kv_heads, page_size, head_dim, dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.empty(pages, kv_heads, page_size // TERN_KV_BLOCK, dtype=torch.float32, device=device)
+                  for _ in range(2)]
+        return KvCache(*codes, *scales)
+
+
+class KvBatch:
+    """The sequences of a call: row_start int32 [batch + 1], kv_len int32 [batch] (tokens in the cache,
+    the call's rows among them), page_table int32 [batch, max_pages], and how many rows there are. The
+    tensors' contents may change between calls and between replays of a captured one."""
+
+    def __init__(self, row_start, kv_len, page_table, rows: int):
+        import torch
+        i32 = (torch.int32,)
+        _want(kv_len, "kv_len", i32, (None,))
+        self.batch, self.rows, self.device = int(kv_len.shape[0]), int(rows), kv_len.device
+        _want(row_start, "row_start", i32, (self.batch + 1,), self.device)
+        _want(page_table, "page_table", i32, (self.batch, None), self.device)
+        self.row_start, self.kv_len, self.page_table = row_start, kv_len, page_table
+        self._c = _KvBatch(self.batch, self.rows, int(page_table.shape[1]), _ptr(row_start), _ptr(kv_len), _ptr(page_table))
+        self._ref = ctypes.byref(self._c)
+
+
+def _heads_out(t, what, rows, heads, head_dim, device):
+    import torch
+    if t.dtype is not torch.bfloat16 or t.device != device or not t.is_contiguous() or t.numel() != rows * heads * head_dim:
+        raise ValueError(f"{what}: expected contiguous bfloat16 [{rows}, {heads}, {head_dim}] on {device}")
+    return t.data_ptr()
+
+
+def _on(device):
+    import torch
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}: make it the current device for the call")
+
+
+def _flag(err_flag, device):
+    import torch
+    if err_flag is None:
+        return None
+    if err_flag.dtype is not torch.int32 or err_flag.device != device:
+        raise ValueError(f"err_flag: expected int32 on {device}")
+    return err_flag.data_ptr()
+
+
+def tern_qk_norm_rope(spec: QkvSpec, src, pos, q, k, flags: int = 0, stream=None) -> None:
+    """Norm and rotation of the q and k heads of src [rows, >= (q_heads + kv_heads) * head_dim] (fp32 or
+    bf16) at positions pos (int32 [rows]) into bf16 q [rows, q_heads, head_dim] and k [rows, kv_heads,
+    head_dim]."""
+    import torch
+    _on(spec.device)
+    rows, D = src.shape[0], spec.head_dim
+    _want(pos, "pos", (torch.int32,), (rows,), spec.device)
+    c = spec._at(src, 1)
+    _check(lib().tern_qk_norm_rope(ctypes.byref(c), rows, pos.data_ptr(), _heads_out(q, "q", rows, spec.q_heads, D, spec.device),
+                                   _heads_out(k, "k", rows, spec.kv_heads, D, spec.device), flags, _stream(stream)),
+           "tern_qk_norm_rope")
+
+
+def tern_kv_append(spec: QkvSpec, src, cache: KvCache, batch: KvBatch, q, err_flag=None, flags: int = 0, stream=None) -> None:
+    """Append the keys and values of src [rows, >= (q_heads + 2 kv_heads) * head_dim] (fp32 or bf16) to the
+    cache and write the rows' queries to q, bf16 [rows, q_heads, head_dim]. err_flag: optional int32
+    tensor, set nonzero for sequences or pages the call has to leave out (never cleared here)."""
+    _on(spec.device)
+    if cache.device != spec.device or batch.device != spec.device:
+        raise ValueError("spec, cache and batch on different devices")
+    if src.shape[0] != batch.rows:
+        raise ValueError(f"src: {src.shape[0]} rows, the batch has {batch.rows}")
+    c = spec._at(src, 2)
+    _check(lib().tern_kv_append(ctypes.byref(c), cache._ref, batch._ref,
+                                _heads_out(q, "q", batch.rows, spec.q_heads, spec.head_dim, spec.device),
+                                _flag(err_flag, spec.device), flags, _stream(stream)), "tern_kv_append")
+
+
+def tern_kv_read(cache: KvCache, batch: KvBatch, k, v, err_flag=None, stream=None) -> None:
+    """The rows' tokens out of the cache: bf16 k and v [rows, kv_heads, head_dim]."""
+    _on(cache.device)
+    if batch.device != cache.device:
+        raise ValueError("cache and batch on different devices")
+    _check(lib().tern_kv_read(cache._ref, batch._ref, _heads_out(k, "k", batch.rows, cache.kv_heads, cache.head_dim, cache.device),
+                              _heads_out(v, "v", batch.rows, cache.kv_heads, cache.head_dim, cache.device),
+                              _flag(err_flag, cache.device), _stream(stream)), "tern_kv_read")
+
+
+def tern_paged_attn_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().tern_paged_attn_workspace_bytes(q_heads, kv_heads, head_dim))
+
+
+def tern_paged_attn(q, scale: float, cache: KvCache, batch: KvBatch, out, workspace, max_rows: int = 1, lse=None,
+                    err_flag=None, flags: int = 0, stream=None) -> None:
+    """Causal attention of bf16 q [rows, q_heads, head_dim] over the cache into bf16 out (same shape) and,
+    if given, fp32 lse [rows, q_heads]. workspace: a zero-filled uint8 CUDA tensor of at least
+    tern_paged_attn_workspace_bytes(...) bytes, one per stream of calls. max_rows: the largest number of
+    rows a sequence is expected to bring (any value is right; it picks the kernel)."""
+    import torch
+    _on(cache.device)
+    if batch.device != cache.device or workspace.device != cache.device:
+        raise ValueError("cache, batch and workspace on different devices")
+    if q.dim() != 3:
+        raise ValueError("q: expected bfloat16 [rows, q_heads, head_dim]")
+    Hq = q.shape[1]
+    if lse is not None and (lse.dtype is not torch.float32 or lse.device != cache.device or not lse.is_contiguous()
+                            or lse.numel() != batch.rows * Hq):
+        raise ValueError(f"lse: expected contiguous float32 [{batch.rows}, {Hq}] on {cache.device}")
+    _check(lib().tern_paged_attn(_heads_out(q, "q", batch.rows, Hq, cache.head_dim, cache.device), Hq, scale, cache._ref,
+                                 batch._ref, max_rows, _heads_out(out, "out", batch.rows, Hq, cache.head_dim, cache.device),
+                                 _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 _flag(err_flag, cache.device), flags, _stream(stream)), "tern_paged_attn")

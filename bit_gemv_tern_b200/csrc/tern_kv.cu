@@ -1,0 +1,311 @@
+// Queries, keys and values between the q|k|v linear and attention: per-head RMSNorm, rotation, and
+// the append to (and read-back from) the paged int8 cache. The formulas and the cache layout are in
+// include/tern.h.
+//
+// k_qkv: one pass over the linear's output rows. A CTA takes a window of rows; a unit is the run of
+// rows that fall into one 16-token block of one sequence (without a cache: the window itself).
+// The unit's rotation angles are the same for every head, so the CTA computes their sines and
+// cosines once into shared memory, and its warps then take heads in turn: a query head streams
+// its rows through; a key or value head holds its up to 16 rows in registers, because the block's
+// scale (an absmax over all of them) must be known before the first code. A lane holds the same
+// D/64 elements of both halves of a head, so the rotation needs no exchange between lanes.
+// One warp owns one (block, head): no atomics, and the result does not depend on the schedule.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "tern_device.cuh"
+#include "tern_kv.cuh"
+#include "tern_kv.h"
+
+namespace tern {
+namespace {
+
+constexpr int kQkvThreads = 256;
+constexpr int kWindow = 16;                     // rows of a window (decode batches take windows of one row)
+constexpr int kReadWindow = 16;
+
+// One head's elements of a lane: lane * V .. of the first half and of the second half.
+template <int V>
+struct Halves {
+  float lo[V], hi[V];
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ Halves<D / 64> load_head(const void* src, int64_t at, int lane) {
+  constexpr int V = D / 64;
+  Halves<V> h;
+  if constexpr (BF16) {
+    const uint16_t* s = static_cast<const uint16_t*>(src) + at + lane * V;
+    if constexpr (V == 2) {
+      const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(s)), b = __ldg(reinterpret_cast<const uint32_t*>(s + D / 2));
+      h.lo[0] = bf16_bits_to_float(a & 0xFFFFu);
+      h.lo[1] = __uint_as_float(a & 0xFFFF0000u);
+      h.hi[0] = bf16_bits_to_float(b & 0xFFFFu);
+      h.hi[1] = __uint_as_float(b & 0xFFFF0000u);
+    } else {
+      h.lo[0] = bf16_bits_to_float(__ldg(s));
+      h.hi[0] = bf16_bits_to_float(__ldg(s + D / 2));
+    }
+  } else {
+    const float* s = static_cast<const float*>(src) + at + lane * V;
+    if constexpr (V == 2) {
+      const float2 a = __ldg(reinterpret_cast<const float2*>(s)), b = __ldg(reinterpret_cast<const float2*>(s + D / 2));
+      h.lo[0] = a.x; h.lo[1] = a.y;
+      h.hi[0] = b.x; h.hi[1] = b.y;
+    } else {
+      h.lo[0] = __ldg(s);
+      h.hi[0] = __ldg(s + D / 2);
+    }
+  }
+  return h;
+}
+
+template <int V>
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Norm (where there is a gain), then rotation by this lane's cosines and sines.
+template <int D>
+__device__ __forceinline__ void norm_rope(Halves<D / 64>& h, const Halves<D / 64>& g, bool norm, float eps,
+                                          const float2* tab) {
+  constexpr int V = D / 64;
+  float r = 1.0f;
+  if (norm) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) ss += h.lo[e] * h.lo[e] + h.hi[e] * h.hi[e];
+    ss = warp_sum<V>(ss);
+    r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float a = norm ? h.lo[e] * r * g.lo[e] : h.lo[e], b = norm ? h.hi[e] * r * g.hi[e] : h.hi[e];
+    const float2 t = tab[e];
+    h.lo[e] = a * t.x - b * t.y;
+    h.hi[e] = b * t.x + a * t.y;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_bf16(uint16_t* dst, const Halves<D / 64>& h, int lane) {
+  constexpr int V = D / 64;
+  if constexpr (V == 2) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(h.lo[0], h.lo[1]), b = __floats2bfloat162_rn(h.hi[0], h.hi[1]);
+    *reinterpret_cast<__nv_bfloat162*>(dst + lane * 2) = a;
+    *reinterpret_cast<__nv_bfloat162*>(dst + D / 2 + lane * 2) = b;
+  } else {
+    *reinterpret_cast<__nv_bfloat16*>(dst + lane) = __float2bfloat16_rn(h.lo[0]);
+    *reinterpret_cast<__nv_bfloat16*>(dst + D / 2 + lane) = __float2bfloat16_rn(h.hi[0]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ Halves<D / 64> load_gain(const uint16_t* gain, int lane) {
+  if (gain) return load_head<D, true>(gain, 0, lane);
+  return Halves<D / 64>{};
+}
+
+// The codes of one token in one block: a lane's 2V codes leave as one store, after neighbours have
+// traded halves (the even lane writes the first half's, the odd lane the second half's).
+template <int D>
+__device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 64>& h, float s, int lane) {
+  constexpr int V = D / 64;
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    lo |= (uint32_t)(quant_i8(h.lo[e], s) & 0xFF) << (8 * e);
+    hi |= (uint32_t)(quant_i8(h.hi[e], s) & 0xFF) << (8 * e);
+  }
+  const bool odd = lane & 1;
+  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+  const uint32_t w = odd ? (got | (hi << (8 * V))) : (lo | (got << (8 * V)));
+  int8_t* at = dst + (odd ? D / 2 : 0) + (lane >> 1) * 2 * V;
+  if constexpr (V == 2) *reinterpret_cast<uint32_t*>(at) = w;
+  else *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+}
+
+// A key or value head of one unit: cnt rows from `row`, at places first .. first + cnt - 1 of the block.
+template <int D, bool BF16>
+__device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int hk, int row, int cnt, int first, int page,
+                                            int place, const float2 (*tab)[D / 2], int lane) {
+  constexpr int V = D / 64;
+  const KvView& kv = p.kv;
+  const int head = p.q_heads + (is_k ? 0 : kv.kv_heads) + hk;
+  Halves<V> x[TERN_KV_BLOCK];
+#pragma unroll
+  for (int j = 0; j < TERN_KV_BLOCK; ++j)
+    if (j < cnt) x[j] = load_head<D, BF16>(p.src, (int64_t)(row + j) * p.stride + (int64_t)head * D, lane);
+  const int64_t blk = ((int64_t)page * kv.kv_heads + hk) * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK;
+  float* scale = (is_k ? kv.ks : kv.vs) + blk;
+  int8_t* codes = (is_k ? kv.k : kv.v) + blk * (TERN_KV_BLOCK * D);
+  const float old = first ? *scale : 0.0f;
+  if (is_k) {
+    const Halves<V> g = load_gain<D>(p.k_gain, lane);
+#pragma unroll
+    for (int j = 0; j < TERN_KV_BLOCK; ++j)
+      if (j < cnt) norm_rope<D>(x[j], g, p.k_gain != nullptr, p.eps, &tab[j][lane * V]);
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < TERN_KV_BLOCK; ++j)
+    if (j < cnt) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) top = fmaxf(top, fmaxf(fabsf(x[j].lo[e]), fabsf(x[j].hi[e])));
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const float s = fmaxf(fmaxf(old, __fdiv_rn(top, 127.0f)), kKvScaleFloor);
+  if (first && s != old) {
+    // the block's scale grows: its earlier codes move to the new one (D/32 bytes of a token per lane)
+    const float f = __fdiv_rn(old, s);
+    for (int j = 0; j < first; ++j) {
+      int8_t* c = codes + j * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) c[e] = (int8_t)__float2int_rn((float)c[e] * f);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < TERN_KV_BLOCK; ++j)
+    if (j < cnt) store_codes<D>(codes + (first + j) * D, x[j], s, lane);
+  if (lane == 0 && s != old) *scale = s;
+}
+
+template <int D, bool BF16, bool APPEND, int W>
+__global__ void __launch_bounds__(kQkvThreads) k_qkv(const __grid_constant__ QkvParams p) {
+  constexpr int V = D / 64;
+  __shared__ float2 tab[kWindow][D / 2];
+  __shared__ int seq[W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w0 = blockIdx.x * W, wn = min(W, p.rows - w0);
+  const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
+  pdl_wait();
+  pdl_launch_dependents();
+  if constexpr (APPEND) locate_rows<kQkvThreads>(p.kv, w0, wn, true, seq);
+  for (int i = 0; i < wn; i += APPEND ? 1 : W) {
+    int row = w0 + i, cnt = wn, pos0 = 0, b = 0;
+    if constexpr (APPEND) {
+      b = seq[i];
+      if (b < 0) continue;
+      const int start = __ldg(p.kv.row_start + b), end = __ldg(p.kv.row_start + b + 1);
+      pos0 = __ldg(p.kv.kv_len + b) - (end - row);
+      if (row != start && pos0 % TERN_KV_BLOCK) continue;       // inside a unit that began earlier
+      cnt = min(TERN_KV_BLOCK - pos0 % TERN_KV_BLOCK, end - row);
+      __syncthreads();                                          // the last unit's table is done with
+    }
+    // angles in turns, reduced in fp64; the sine and cosine of the remainder in fp32
+    for (int t = threadIdx.x; t < cnt * (D / 2); t += kQkvThreads) {
+      const int j = t / (D / 2), e = t % (D / 2);
+      const double pos = APPEND ? (double)(pos0 + j) : (double)__ldg(p.pos + row + j);
+      double turn = pos * (__ldg(p.freq + e) * 0.15915494309189533577);
+      turn -= rint(turn);
+      float s, c;
+      sincospif(2.0f * (float)turn, &s, &c);
+      tab[j][e] = make_float2(c, s);
+    }
+    __syncthreads();
+    int page = 0, place = 0;
+    if constexpr (APPEND) {
+      page = __ldg(p.kv.table + (int64_t)b * p.kv.max_pages + pos0 / p.kv.page_size);
+      place = pos0 % p.kv.page_size;
+      if (page < 0 || page >= p.kv.pages) {
+        if (threadIdx.x == 0 && p.kv.flag) *p.kv.flag = 1;
+        page = -1;
+      }
+    }
+    for (int t = blockIdx.y * (kQkvThreads / 32) + warp; t < tasks; t += gridDim.y * (kQkvThreads / 32)) {
+      if constexpr (APPEND) {
+        if (t < 2 * p.kv_heads) {
+          if (page >= 0)
+            append_head<D, BF16>(p, t < p.kv_heads, t % p.kv_heads, row, cnt, place % TERN_KV_BLOCK, page, place, tab, lane);
+          continue;
+        }
+      }
+      const int h = APPEND ? t - 2 * p.kv_heads : t;            // source head: queries, then keys
+      const bool is_q = h < p.q_heads;
+      const uint16_t* gain = is_q ? p.q_gain : p.k_gain;
+      const Halves<V> g = load_gain<D>(gain, lane);
+      uint16_t* dst = is_q ? p.q + ((int64_t)row * p.q_heads + h) * D : p.k + ((int64_t)row * p.kv_heads + h - p.q_heads) * D;
+      const int64_t step = (int64_t)(is_q ? p.q_heads : p.kv_heads) * D;
+#pragma unroll 4
+      for (int j = 0; j < cnt; ++j) {
+        Halves<V> x = load_head<D, BF16>(p.src, (int64_t)(row + j) * p.stride + (int64_t)h * D, lane);
+        norm_rope<D>(x, g, gain != nullptr, p.eps, &tab[j][lane * V]);
+        store_bf16<D>(dst + j * step, x, lane);
+      }
+    }
+  }
+}
+
+// Eight elements of one token and head per thread and step: 8 code bytes in, 16 bytes out.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadParams p) {
+  __shared__ int seq[kReadWindow];
+  const KvView& kv = p.kv;
+  const int w0 = blockIdx.x * kReadWindow, wn = min(kReadWindow, kv.rows - w0);
+  locate_rows<256>(kv, w0, wn, true, seq);
+  const int per_row = kv.kv_heads * (D / 8);
+  for (int t = threadIdx.x; t < wn * per_row * 2; t += 256) {
+    const bool is_v = t >= wn * per_row;
+    const int u = is_v ? t - wn * per_row : t;
+    const int i = u / per_row, hk = u % per_row / (D / 8), c = u % (D / 8), b = seq[i], row = w0 + i;
+    if (b < 0) continue;
+    const int pos = __ldg(kv.kv_len + b) - (__ldg(kv.row_start + b + 1) - row);
+    const int page = __ldg(kv.table + (int64_t)b * kv.max_pages + pos / kv.page_size);
+    if (page < 0 || page >= kv.pages) {
+      if (kv.flag) *kv.flag = 1;
+      continue;
+    }
+    const int place = pos % kv.page_size;
+    const int64_t head = (int64_t)page * kv.kv_heads + hk;
+    const float s = (is_v ? kv.vs : kv.ks)[head * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK];
+    const uint2 w = *reinterpret_cast<const uint2*>((is_v ? kv.v : kv.k) + (head * kv.page_size + place) * D + c * 8);
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = (e < 2 ? w.x : w.y) >> (16 * (e & 1));
+      const __nv_bfloat162 v = __floats2bfloat162_rn((float)(int8_t)(x & 0xFF) * s, (float)(int8_t)((x >> 8) & 0xFF) * s);
+      o[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((int64_t)row * kv.kv_heads + hk) * D + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+template <int D, bool BF16, bool APPEND>
+cudaError_t launch_qkv_t(const QkvParams& p, bool pdl, cudaStream_t st) {
+  // windows of one row while the sequences bring fewer than 16 rows each (decode, verify), so that
+  // every block is a CTA's own; windows of 16 rows for longer runs, whose blocks fill up
+  const bool wide = APPEND ? p.rows / p.kv.batch >= kWindow : p.rows >= 64 * kWindow;
+  const int windows = wide ? (p.rows + kWindow - 1) / kWindow : p.rows;
+  const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
+  const int warps = kQkvThreads / 32;
+  // split the heads over CTAs until every SM has two
+  int split = (2 * device_sm_count() + windows - 1) / windows;
+  if (split > (tasks + warps - 1) / warps) split = (tasks + warps - 1) / warps;
+  const dim3 grid(windows, split);
+  return wide ? launch_maybe_pdl(k_qkv<D, BF16, APPEND, kWindow>, grid, dim3(kQkvThreads), 0, pdl, st, p)
+              : launch_maybe_pdl(k_qkv<D, BF16, APPEND, 1>, grid, dim3(kQkvThreads), 0, pdl, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_qkv(const QkvParams& p, int head_dim, bool bf16, bool append, bool pdl, cudaStream_t st) {
+  if (head_dim == 128) {
+    if (append) return bf16 ? launch_qkv_t<128, true, true>(p, pdl, st) : launch_qkv_t<128, false, true>(p, pdl, st);
+    return bf16 ? launch_qkv_t<128, true, false>(p, pdl, st) : launch_qkv_t<128, false, false>(p, pdl, st);
+  }
+  if (append) return bf16 ? launch_qkv_t<64, true, true>(p, pdl, st) : launch_qkv_t<64, false, true>(p, pdl, st);
+  return bf16 ? launch_qkv_t<64, true, false>(p, pdl, st) : launch_qkv_t<64, false, false>(p, pdl, st);
+}
+
+cudaError_t launch_kv_read(const KvReadParams& p, int head_dim, cudaStream_t st) {
+  const int grid = (p.kv.rows + kReadWindow - 1) / kReadWindow;
+  if (head_dim == 128) k_kv_read<128><<<grid, 256, 0, st>>>(p);
+  else k_kv_read<64><<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace tern

@@ -1,0 +1,80 @@
+// Launch interface of the attention-side kernels: per-head norm and rotation, the paged int8
+// key/value cache, attention over it (declared for callers in include/tern.h).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/tern.h"
+
+namespace tern {
+
+// A cache and the sequences of a call, as the kernels take them.
+struct KvView {
+  int8_t* k;
+  int8_t* v;
+  float* ks;
+  float* vs;
+  int32_t pages, page_size, kv_heads;
+  int32_t batch, rows, max_pages;
+  const int32_t* row_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int32_t* flag;               // optional error flag
+};
+
+struct QkvParams {
+  const void* src;
+  int64_t stride;              // elements
+  int32_t q_heads, kv_heads;
+  const uint16_t* q_gain;
+  const uint16_t* k_gain;
+  float eps;
+  const double* freq;
+  const int32_t* pos;          // without a cache
+  uint16_t* q;
+  uint16_t* k;                 // without a cache
+  int32_t rows;
+  KvView kv;                   // with a cache
+};
+// bf16: source type; append: into the cache, else to q and k rows.
+cudaError_t launch_qkv(const QkvParams& p, int head_dim, bool bf16, bool append, bool pdl, cudaStream_t st);
+
+struct KvReadParams {
+  KvView kv;
+  uint16_t* k;
+  uint16_t* v;
+};
+cudaError_t launch_kv_read(const KvReadParams& p, int head_dim, cudaStream_t st);
+
+struct AttnParams {
+  KvView kv;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;                  // optional
+  int32_t q_heads, group;      // group = q_heads / kv_heads
+  float scale;
+  int32_t max_rows;
+  uint8_t* ws;
+};
+size_t attn_workspace_bytes(int head_dim);
+cudaError_t launch_attn(const AttnParams& p, int head_dim, bool pdl, cudaStream_t st);
+
+// One launch, optionally with programmatic stream serialisation (the kernel calls pdl_wait()).
+template <typename P>
+cudaError_t launch_maybe_pdl(void (*kern)(P), dim3 grid, dim3 block, size_t smem, bool pdl, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace tern

@@ -49,7 +49,8 @@
  *     tern_occupancy, tern_quantize_act,
  *     the prologues (tern_gemm_batch_pro, tern_act_prologue), the verify round (i8_head_verify,
  *     tern_verify_accept), the five-valued blocks (tern_fv5_*, fv5b_head_gemv_argmax), the dependent chain
- *     (tern_chain_*) and i8_head_gemv_argmax_noalloc are additions.
+ *     (tern_chain_*), the attention-side operators (tern_qk_norm_rope, tern_kv_*, tern_paged_attn) and
+ *     i8_head_gemv_argmax_noalloc are additions.
  *
  * Packed layout (this library's own; the pages' FV5 bit-planes are only partly described)
  *   Matrix N x K, K a multiple of 128. Row n occupies K/16 uint32 words at word offset n*K/16:
@@ -520,6 +521,130 @@ tern_status fv5b_head_gemv_argmax(const int8_t* W_dev, const float* block_scale_
                                   tern_act act, const void* X_dev, const float* x_scale_dev, int32_t* argmax_dev,
                                   float* maxval_dev, float* logits_dev, void* workspace_dev, size_t workspace_bytes,
                                   tern_stream_t stream);
+
+/* ---- Between the q|k|v linear and the o linear: norms, rotation, paged 8-bit cache, attention ----
+ *
+ * The Qwen3 block of the Neutrino-1 models ([R] "세 모델과 하나의 컨테이너", model table: grouped
+ * query heads, per-head RMSNorm of q and k, rotation with base 1e6, heads of 128) puts these steps
+ * between two of its linears. They read the fused q|k|v linear's output and leave the bf16
+ * activation rows that the o linear takes (K = q_heads * head_dim).
+ *
+ * Cache: keys and values are held as int8 codes with one fp32 scale for every 16 tokens of a head
+ * (a block); a value is code * scale. Pages hold page_size tokens of every head, so a block never
+ * crosses a page and one head's tokens of a page are contiguous:
+ *   codes  int8 [pages][kv_heads][page_size][head_dim]
+ *   scales fp32 [pages][kv_heads][page_size / 16]
+ * Token t of a sequence sits in page page_table[sequence][t / page_size] at place t % page_size.
+ * A sequence's cache costs 2 * kv_heads * (head_dim + 1/4) bytes per token (half of bf16).
+ *
+ * Rows: a call works on `rows` activation rows; sequence b owns rows row_start[b] .. row_start[b + 1)
+ * (n_b of them, none is allowed), and its row i is token kv_len[b] - n_b + i: kv_len counts the
+ * tokens in the cache with this call's own among them. Rows behind the last sequence belong to
+ * nobody: they are not read and their outputs are left as they were.
+ *
+ * row_start, kv_len and page_table live on the device and may change between the replays of a
+ * captured call. What only the device can see of them is checked there: a sequence with row_start
+ * decreasing or outside 0 .. rows, or with kv_len negative or past max_pages * page_size, is left
+ * out (its outputs stay as they were), a page outside 0 .. pages - 1 is neither read nor written
+ * (its tokens are not seen, its rows are not returned), and *err_flag_dev, if given, is set
+ * nonzero. The flag is never cleared by these calls (clear it once; tern_read_flag reads it).
+ * Pages that two sequences share may be read by both; no two sequences of a call may append into
+ * one page. */
+typedef enum { TERN_ELEM_F32 = 0, TERN_ELEM_BF16 = 1 } tern_elem;
+
+/* Tokens that share one scale. */
+#define TERN_KV_BLOCK 16
+
+typedef struct {
+  int32_t pages;              /* pages in the cache, >= 1                                       */
+  int32_t page_size;          /* tokens per page, a multiple of 16, 16 .. 65536                 */
+  int32_t kv_heads;           /* 1 .. 1024                                                      */
+  int32_t head_dim;           /* 64 or 128                                                      */
+  int8_t* k_dev;              /* codes, 16-byte aligned                                         */
+  int8_t* v_dev;
+  float* k_scale_dev;         /* scales, 4-byte aligned                                         */
+  float* v_scale_dev;
+} tern_kv_cache;
+
+typedef struct {
+  int32_t batch;                  /* sequences, 1 .. 65536                                      */
+  int32_t rows;                   /* activation rows, 0 .. 2^24 (0: nothing is enqueued)        */
+  int32_t max_pages;              /* entries per page_table row; max_pages * page_size < 2^31   */
+  const int32_t* row_start_dev;   /* [batch + 1]                                                */
+  const int32_t* kv_len_dev;      /* [batch]                                                    */
+  const int32_t* page_table_dev;  /* [batch][max_pages]                                         */
+} tern_kv_batch;
+
+/* Rows of a q|k|v output and what turns them into queries and keys: per head vector x,
+ *   z = x * r * gain, r = 1 / sqrt(sum x^2 / head_dim + eps)      (gain NULL: z = x, no norm)
+ *   y_i = z_i cos a_i - z_(i + D/2) sin a_i,  y_(i + D/2) = z_(i + D/2) cos a_i + z_i sin a_i,
+ * a_i = position * freq[i], i < D/2 = head_dim / 2. Norm and rotation are in fp32, the angle is
+ * reduced in fp64 (exact to 1e-9 of a turn at every position an int32 holds), and a result is
+ * rounded once: to bf16 (q, and k outside the cache) or to its int8 code. Values are left alone.
+ * Inputs are finite. */
+typedef struct {
+  const void* src_dev;          /* [rows][row_stride]: q heads, k heads, v heads; 16-byte aligned */
+  int32_t src_type;             /* tern_elem                                                    */
+  int32_t q_heads, kv_heads;    /* q_heads a multiple of kv_heads, at most 4096                 */
+  int32_t head_dim;             /* 64 or 128                                                    */
+  int64_t row_stride;           /* elements between rows: a multiple of 4, at least a row       */
+  const uint16_t* q_gain_dev;   /* bf16 [head_dim] or NULL, 4-byte aligned                      */
+  const uint16_t* k_gain_dev;
+  float eps;                    /* finite, >= 0                                                 */
+  const double* freq_dev;       /* [head_dim / 2] radians per position, 8-byte aligned          */
+} tern_qkv;
+
+/* Norm and rotation without a cache: rows of q and k (row_stride >= (q_heads + kv_heads) *
+ * head_dim) at positions pos_dev (int32 [rows], >= 0) into q_dev bf16 [rows][q_heads][head_dim] and
+ * k_dev bf16 [rows][kv_heads][head_dim] (16-byte aligned, neither overlapping the source). */
+tern_status tern_qk_norm_rope(const tern_qkv* x, int32_t rows, const int32_t* pos_dev, uint16_t* q_dev,
+                              uint16_t* k_dev, uint32_t flags, tern_stream_t stream);
+
+/* Append the rows' keys (normalised, rotated) and values to the cache, and write the rows' queries
+ * (normalised, rotated) to q_dev, bf16 [rows][q_heads][head_dim], 16-byte aligned. Every block that
+ * receives tokens gets the scale
+ *   s = max(s_old, absmax of its new values / 127, 2^-60)
+ * where s_old is the block's scale if it holds earlier tokens of the sequence, else 0 (what lies in a
+ * fresh block is not looked at); where s grows, the earlier codes become rint(code * (s_old / s)).
+ * New codes are clamp(rint(value / s), -127, 127). Appending the same rows at the same place
+ * again leaves the cache as it is, so a call may be repeated, and after a rejected draft the
+ * next call simply comes with a smaller kv_len.
+ * flags: 0 or TERN_FLAG_PDL (the kernel waits for the preceding one before it reads anything). */
+tern_status tern_kv_append(const tern_qkv* x, const tern_kv_cache* cache, const tern_kv_batch* batch,
+                           uint16_t* q_dev, int32_t* err_flag_dev, uint32_t flags, tern_stream_t stream);
+
+/* Read tokens back: for every row its token's keys and values, code * scale rounded to bf16, into
+ * k_dev and v_dev, bf16 [rows][kv_heads][head_dim], 16-byte aligned. */
+tern_status tern_kv_read(const tern_kv_cache* cache, const tern_kv_batch* batch, uint16_t* k_dev, uint16_t* v_dev,
+                         int32_t* err_flag_dev, tern_stream_t stream);
+
+/* Workspace bytes of tern_paged_attn, whatever the batch and the lengths (0 if the heads are invalid). */
+size_t tern_paged_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+
+/* Attention over the cache. Query head h reads key/value head h / (q_heads / kv_heads); a row at
+ * position p sees the tokens 0 .. p of its sequence (so the rows of one call see each other
+ * causally, and appending comes first):
+ *   s_j = softmax_scale * (q . k_j),  out = sum_j e^(s_j) v_j / sum_j e^(s_j),  lse = ln sum_j e^(s_j)
+ * out_dev bf16 [rows][q_heads][head_dim]; lse_dev optional fp32 [rows][q_heads]. A row that sees
+ * nothing (kv_len < n_b) gives out = 0 and lse = -infinity.
+ *   q_dev bf16 [rows][q_heads][head_dim]; q, out 16-byte aligned, not overlapping; q_heads a
+ *   multiple of cache->kv_heads, at most 4096; softmax_scale finite.
+ *   max_rows: the largest n_b the caller expects (>= 1). It only chooses between the kernels (one that
+ *   streams the cache for a few rows a sequence, one that multiplies large tiles); any value
+ *   gives the right result.
+ *   workspace_dev: at least tern_paged_attn_workspace_bytes bytes, 16-byte aligned, zero-filled
+ *   before its first use; every call leaves its counters zero again, so one buffer serves any number of
+ *   calls in stream order (two calls, or two captured graphs, that overlap in time need two).
+ * Codes and queries are multiplied exactly (the queries as fp16 scaled by a power of two of
+ * their row's absmax), sums, maxima and the softmax are fp32, the probabilities times the value
+ * block's scale are rounded to fp16 for the second product. |value| below 2^27 keeps that scaling
+ * exact. Results do not depend on the run, but on the other sequences of the call through the way
+ * the work is split (within rounding).
+ * flags: 0 or TERN_FLAG_PDL (the kernel waits for the preceding one before it reads anything). */
+tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softmax_scale, const tern_kv_cache* cache,
+                            const tern_kv_batch* batch, int32_t max_rows, uint16_t* out_dev, float* lse_dev,
+                            void* workspace_dev, size_t workspace_bytes, int32_t* err_flag_dev, uint32_t flags,
+                            tern_stream_t stream);
 
 /* Synchronise `stream`, read *err_flag_dev and map it: 0 -> TERN_OK, nonzero -> TERN_EBADCODE. */
 tern_status tern_read_flag(const int32_t* err_flag_dev, tern_stream_t stream);
