@@ -1,76 +1,672 @@
-// Attention over the paged int8 cache (include/tern.h, tern_paged_attn).
+// Attention over the paged int8 cache for a few rows a sequence (decode tokens, draft-verify rows):
+// include/tern.h, tern_paged_attn.
 //
-// One warp per row and query head walks the row's tokens with the running maximum and sum of the
-// softmax; a lane holds D/32 elements of the head.
+//   s_j = scale * q.k_j,  out = sum_j e^(s_j) v_j / sum_j e^(s_j)
+//
+// Bound by the cache's bytes: every key and value code is read once and used for the `group`
+// query heads (times the sequence's rows) that share it. One persistent CTA per SM streams the cache
+// through a ring of shared-memory stages (TMA, one box per 16-token block, 128-byte swizzle), whatever
+// sequence, head and page the tokens belong to:
+//
+//   Work.   A tile is R query rows (row x head of the group, flattened) of one sequence and one
+//           key/value head; its chunks are the 64-token stages that its last row sees. The chunks of all
+//           tiles, in order, are cut into equal contiguous ranges, one per CTA, found on the device
+//           from kv_len and row_start (a captured call follows the lengths). A tile that spans CTAs
+//           leaves a partial result (max, sum, unnormalised output) per CTA in the workspace; the last
+//           CTA to arrive, by a counter, joins them in CTA order, so results do not depend on timing.
+//   Warps.  One producer warp; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
+//           of its own (max, sum, output in registers); the warps' results are joined once per tile.
+//   Math.   S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 f16: the 16 tokens of a block are the
+//           M side of the first product, so a block's scale is one number per instruction, and the
+//           query rows are the N side, 8 at a time (a decode token of a group of four wastes half of
+//           it, not three quarters as on the M side). Codes become fp16 exactly (0x6400 | byte is
+//           1024 + byte). tcgen05 would need M = 128 rows or tokens as the wide operand; at these row
+//           counts the tensor pipe is mostly idle and the bytes bind.
+//   Scales. The exponent of a probability carries the value block's scale, e = log2(e) s + log2(s_v):
+//           p' = 2^(e - max e) is the fp16 operand of the second product and never above 2^8,
+//           whatever the scales; the softmax's sum is sum p' / s_v in fp32.
 #include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "tern_device.cuh"
+#include "tern_kernels.h"
 #include "tern_kv.cuh"
 #include "tern_kv.h"
+#include "tern_mbar.cuh"
 
 namespace tern {
+
+__device__ int g_attn_latch = 0;
+
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) k_attn_rows(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32;
-  __shared__ int seq[1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x;
-  pdl_wait();
-  locate_rows<128>(p.kv, row, 1, false, seq);
-  const int b = seq[0];
-  if (b < 0) return;
-  const SeqInfo si = seq_info(p.kv, b);
-  const int pos = si.len - (si.start + si.n - row);
-  for (int h = blockIdx.y * 4 + warp; h < p.q_heads; h += gridDim.y * 4) {
-    const int hk = h / p.group;
-    float q[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[e] = bf16_bits_to_float(p.q[((int64_t)row * p.q_heads + h) * D + lane * E + e]) * p.scale;
-      o[e] = 0.0f;
-    }
-    float m = -INFINITY, l = 0.0f;
-    for (int j = 0; j <= pos; ++j) {
-      const int page = __ldg(p.kv.table + (int64_t)b * p.kv.max_pages + j / p.kv.page_size);
-      if (page < 0 || page >= p.kv.pages) {
-        if (p.kv.flag && lane == 0) *p.kv.flag = 1;
-        continue;
-      }
-      const int place = j % p.kv.page_size;
-      const int64_t head = (int64_t)page * p.kv.kv_heads + hk, at = (head * p.kv.page_size + place) * D + lane * E;
-      const int64_t blk = head * (p.kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK;
-      float s = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s += q[e] * (float)p.kv.k[at + e];
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-      s *= p.kv.ks[blk];
-      const float mn = fmaxf(m, s), f = expf(m - mn), w = expf(s - mn), vs = p.kv.vs[blk];
-      l = l * f + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * (vs * (float)p.kv.v[at + e]);
-      m = mn;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      *reinterpret_cast<__nv_bfloat16*>(p.out + ((int64_t)row * p.q_heads + h) * D + lane * E + e) =
-          __float2bfloat16_rn(l > 0.0f ? o[e] / l : 0.0f);
-    if (p.lse && lane == 0) p.lse[(int64_t)row * p.q_heads + h] = m + logf(l);
+constexpr int kChunk = 64;                        // tokens of a stage: four blocks
+constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
+constexpr float kLog2e = 1.4426950408889634f;
+// The running maximum follows only when it rises by more than this (a power of two of slack in p'
+// instead of a rescale of the output for every small rise).
+constexpr float kSlack = 8.0f;
+
+template <int D, int R>
+struct Shape {
+  // consumer warps; with the producer 16, 12 or 8 warps, four, three or two to a register file
+  // partition: 128, 168 or 255 registers a thread
+  static constexpr int kCW = R == 8 ? 15 : R == 16 ? 11 : 7;
+  static constexpr int kThreads = (kCW + 1) * 32;
+  static constexpr int kNT = R / 8;                               // 8-row column groups
+  static constexpr int kTiles = D / 16;                           // 16-element tiles of a head
+  static constexpr int kHalfStage = kChunk * D;                   // bytes of a stage's keys
+  static constexpr int kStages = (R == 32 ? 4 : 8) * 128 / D;
+  static constexpr int kRowPitch = D + 4;                         // floats of a row in the join buffer
+  // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][2][4] | masks | barriers
+  static constexpr int kOffJoin = kStages * 2 * kHalfStage;
+  static constexpr int kOffMax = kOffJoin + kCW * R * kRowPitch * 4;
+  static constexpr int kOffSum = kOffMax + kCW * R * 4;
+  static constexpr int kOffScale = kOffSum + kCW * R * 4;
+  static constexpr int kOffMask = kOffScale + kStages * 2 * kBlocks * 4;
+  static constexpr int kOffQ = kOffMask + kStages * 4;            // R = 32: query fragments [step][NT][32] x 8 B
+  static constexpr int kOffBar = kOffQ + (R == 32 ? D / 16 * kNT * 256 : 0);
+  static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
+  static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
+  // a range is at least as many chunks as give every consumer warp a block
+  static constexpr int kMinChunks = kCW / kBlocks;
+};
+constexpr int kCounterBytes = 1024;               // one counter per CTA
+
+struct alignas(64) StreamAttn {
+  CUtensorMap kmap, vmap;      // [pages * kv_heads * page_size][head_dim] bytes, boxes of 16 rows
+  AttnParams p;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 16-bit transpose across the warp.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two fp16 codes from two bytes of x, which holds code + 128: SEL 0x4140 takes bytes 0 and 1, 0x4342
+// bytes 2 and 3; 0x6400 | u is 1024 + u, and 1152 comes off again (all exact).
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
+  const uint32_t w = __byte_perm(x, 0x64646464u, SEL);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The walk over tiles: sequence, key/value head, row tile; chunks of a tile.
+template <int R>
+struct Walk {
+  SeqInfo s;
+  int b, hk, qt, chunks, vis;
+  __device__ __forceinline__ static int tiles_of(const SeqInfo& s, int group) { return (s.n * group + R - 1) / R; }
+  // tokens that the last row of a row tile sees
+  __device__ __forceinline__ static int visible(const SeqInfo& s, int group, int qt) {
+    const int last = min(s.n - 1, ((qt + 1) * R - 1) / group);
+    return max(0, s.len - s.n + last + 1);
   }
+  __device__ __forceinline__ static int chunks_of(int vis) { return max(1, (vis + kChunk - 1) / kChunk); }
+  __device__ __forceinline__ static long long chunks_of_head(const SeqInfo& s, int group) {
+    long long sum = 0;
+    const int nt = tiles_of(s, group);
+    for (int q = 0; q < nt; ++q) sum += chunks_of(visible(s, group, q));
+    return sum;
+  }
+  __device__ __forceinline__ void set(int group) {
+    vis = visible(s, group, qt);
+    chunks = chunks_of(vis);
+  }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    if (++qt < tiles_of(s, p.group)) return set(p.group);
+    qt = 0;
+    if (++hk < p.kv.kv_heads) return set(p.group);
+    hk = 0;
+    for (++b; b < p.kv.batch; ++b) {
+      s = seq_info(p.kv, b);
+      if (s.n) return set(p.group);
+    }
+  }
+};
+
+// Where a CTA's range starts.
+struct Plan {
+  long long total, per;
+  int b, hk, qt, off;          // tile and the chunk in it
+};
+
+// Finds this CTA's range of the call's chunks. Every thread takes part.
+template <int R, int kThreadsT>
+__device__ __forceinline__ void make_plan(const AttnParams& p, int min_chunks, Plan* plan, long long* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kThreadsT / 32;
+  auto load = [&](int b) -> long long {
+    if (b >= p.kv.batch) return 0;
+    const SeqInfo s = seq_info(p.kv, b);
+    if (!s.ok) {
+      if (p.kv.flag && blockIdx.x == 0) *p.kv.flag = 1;
+      return 0;
+    }
+    return s.n ? Walk<R>::chunks_of_head(s, p.group) : 0;
+  };
+  long long total = 0;                           // per key/value head
+  long long mine = 0;
+  for (int b = threadIdx.x; b < p.kv.batch; b += kThreadsT) mine += load(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+  if (lane == 0) warp_sums[warp] = mine;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) total += warp_sums[w];
+  total *= p.kv.kv_heads;
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < min_chunks) per = min_chunks;
+  const long long s0 = per * blockIdx.x;
+  if (threadIdx.x == 0) plan->total = total, plan->per = per, plan->b = -1;
+  if (s0 < total) {
+    long long base = 0;                          // chunks of the sequences before this round's
+    for (int b0 = 0; b0 < p.kv.batch; b0 += kThreadsT) {
+      const int b = b0 + threadIdx.x;
+      const long long c = load(b) * p.kv.kv_heads;
+      long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      __syncthreads();
+      if (lane == 31) warp_sums[warp] = incl;
+      __syncthreads();
+      long long before = base, all = base;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+      }
+      before += incl - c;
+      if (c && s0 >= before && s0 < before + c) {
+        const SeqInfo s = seq_info(p.kv, b);
+        const long long per_head = c / p.kv.kv_heads;
+        long long rem = s0 - before;
+        plan->b = b;
+        plan->hk = (int)(rem / per_head);
+        rem %= per_head;
+        int qt = 0;
+        for (;; ++qt) {
+          const int n = Walk<R>::chunks_of(Walk<R>::visible(s, p.group, qt));
+          if (rem < n) break;
+          rem -= n;
+        }
+        plan->qt = qt;
+        plan->off = (int)rem;
+      }
+      base = all;
+      if (s0 < base) break;                      // uniform: s0 and base are
+    }
+  }
+  __syncthreads();
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const __grid_constant__ StreamAttn a) {
+  using SH = Shape<D, R>;
+  constexpr int CW = SH::kCW, NT = SH::kNT, T = SH::kTiles, ST = SH::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base - raw);
+  float* join = reinterpret_cast<float*>(sm + SH::kOffJoin);
+  float* smax = reinterpret_cast<float*>(sm + SH::kOffMax);
+  float* ssum = reinterpret_cast<float*>(sm + SH::kOffSum);
+  float* sscale = reinterpret_cast<float*>(sm + SH::kOffScale);
+  uint32_t* smask = reinterpret_cast<uint32_t*>(sm + SH::kOffMask);
+  const uint32_t full = base + SH::kOffBar, empty = full + 8 * ST;
+  __shared__ Plan plan;
+  __shared__ long long warp_sums[SH::kThreads / 32];
+  __shared__ int s_last;
+  const AttnParams& p = a.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, kBlocks);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  make_plan<R, SH::kThreads>(p, SH::kMinChunks, &plan, warp_sums);   // ends with a barrier
+  const long long per = plan.per, total = plan.total, s0 = per * blockIdx.x;
+  if (s0 >= total) return;
+  const int count = (int)min(per, total - s0);                       // chunks of this CTA
+  Walk<R> w;
+  w.b = plan.b;
+  w.hk = plan.hk;
+  w.qt = plan.qt;
+  w.s = seq_info(p.kv, w.b);
+  w.set(p.group);
+  int off = plan.off;
+  bool ok = true;
+
+  if (warp == CW) {
+    // ---------------- producer: pages, scales and boxes, a group of 32 blocks looked up ahead ----------------
+    struct Group {
+      int row;                 // first row of the block in the tensor maps, -1: no such page, -2: past the end
+      float ks, vs;
+    };
+    auto look = [&](const Walk<R>& x, int chunk0) -> Group {
+      Group g{-2, 0.0f, 0.0f};
+      const int t = chunk0 * kChunk + lane * TERN_KV_BLOCK;
+      if (t < x.vis) {
+        const int page = __ldg(p.kv.table + (int64_t)x.b * p.kv.max_pages + t / p.kv.page_size), place = t % p.kv.page_size;
+        g.row = -1;
+        if (page >= 0 && page < p.kv.pages) {
+          const int head = page * p.kv.kv_heads + x.hk;
+          const int64_t blk = (int64_t)head * (p.kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK;
+          g.row = head * p.kv.page_size + place;
+          g.ks = p.kv.ks[blk];
+          g.vs = p.kv.vs[blk];
+        } else if (p.kv.flag) {
+          *p.kv.flag = 1;
+        }
+      }
+      return g;
+    };
+    constexpr int kAhead = 32 / kBlocks;         // chunks of a group
+    Group cur = look(w, off), nxt = cur;
+    int q = 0, at = 0;                           // ring position; chunk of the group
+    while (q < count && ok) {
+      const int seg = min(w.chunks - off, count - q);
+      for (int c = 0; c < seg; ++c, ++q) {
+        if (at == 0) {                           // look the next group up while this one is copied
+          if (c + kAhead < seg) nxt = look(w, off + c + kAhead);
+          else if (q + seg - c < count) {
+            Walk<R> x = w;
+            x.next(p);
+            nxt = look(x, 0);
+          }
+        }
+        const int s = q % ST;
+        if (q >= ST && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * s, ((q / ST) - 1) & 1)))) break;
+        const int j = lane & (kBlocks - 1), from = at * kBlocks + j;
+        const int row = __shfl_sync(0xFFFFFFFFu, cur.row, from);
+        const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, from), vs = __shfl_sync(0xFFFFFFFFu, cur.vs, from);
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, row >= 0) & ((1u << kBlocks) - 1);
+        if (lane < 2 * kBlocks) sscale[s * 2 * kBlocks + lane] = lane < kBlocks ? ks : vs;
+        if (lane == 0) smask[s] = have;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, __popc(have) * 2 * TERN_KV_BLOCK * D);
+        __syncwarp();
+        if (lane < 2 * kBlocks && row >= 0)
+          tma_load_2d(base + s * 2 * SH::kHalfStage + (lane < kBlocks ? 0 : SH::kHalfStage) + j * TERN_KV_BLOCK * D,
+                      lane < kBlocks ? &a.kmap : &a.vmap, 0, row, full + 8 * s);
+        if (++at == kAhead || c + 1 == seg) {
+          cur = nxt;
+          at = 0;
+        }
+      }
+      if (!ok) break;
+      off = 0;
+      if (q < count) w.next(p);
+    }
+    // do not leave with copies in flight (bounded, also after a give-up)
+    for (int r = q > ST ? q - ST : 0; r < q; ++r)
+      if (!mbar_wait(full + 8 * (r % ST), (r / ST) & 1)) { ok = false; break; }
+    if (!ok && lane == 0) atomicExch(&g_attn_latch, 5);
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int g = lane >> 2, t = lane & 3;
+  const int swz = D == 128 ? (g & 7) : ((g >> 1) & 3);               // row g's (and g + 8's) chunk swizzle
+  int q0 = 0;                                                        // ring position of the segment
+  while (q0 < count) {
+    const int seg = min(w.chunks - off, count - q0);
+    const int rows = min(R, w.s.n * p.group - w.qt * R);             // valid rows of the tile
+    const int row0 = w.qt * R;                                       // flattened: row * group + head
+    // queries as fp16 fragments, each row scaled by a power of two into [2^13, 2^14)
+    uint32_t qf[R == 32 ? 1 : NT][R == 32 ? 1 : T][2];
+    float rowf[NT][2], m[NT][2], l[NT][2], o[T][NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + g;
+      uint4 v[D / 32];
+      float top = 0.0f;
+      const bool live = 8 * n + g < rows;
+      const uint16_t* src = p.q + ((int64_t)(w.s.start + (live ? r / p.group : 0)) * p.q_heads + w.hk * p.group + (live ? r % p.group : 0)) * D + t * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        v[i] = live ? ld_nc(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      int E = (int)(__float_as_uint(top) >> 23) - 126;               // top < 2^E
+      E = max(-100, min(E, 128));
+      const float up = exp2f_i(14 - E);
+      const float f = p.scale * kLog2e * exp2f_i(E - 14);
+      rowf[n][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);               // rows 2t, 2t + 1 of the group of eight
+      rowf[n][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t h = pack_f16(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
+          if constexpr (R == 32) {
+            // step 2i + e/2 of the fragments in shared memory; every warp writes the same
+            uint32_t* sq = reinterpret_cast<uint32_t*>(sm + SH::kOffQ);
+            if (warp == n) sq[(((2 * i + (e >> 1)) * NT + n) * 32 + lane) * 2 + (e & 1)] = h;
+          } else {
+            qf[n][2 * i + (e >> 1)][e & 1] = h;
+          }
+        }
+      }
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < T; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+    }
+    if constexpr (R == 32) named_sync(1, CW * 32);
+    // tokens below this are seen by every row of the tile
+    const int clear = max(0, w.s.len - w.s.n + row0 / p.group + 1);
+    const int phase = (int)(((long long)q0 * kBlocks) % CW);
+
+    for (int i = (warp - phase + CW) % CW; i < seg * kBlocks; i += CW) {
+      const int qs = q0 + i / kBlocks, s = qs % ST, j = i % kBlocks;
+      const int t0 = (off + i / kBlocks) * kChunk + j * TERN_KV_BLOCK;
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * s, (qs / ST) & 1));
+      if (ok && t0 < w.vis && (smask[s] >> j & 1)) {
+        const uint32_t kb = base + s * 2 * SH::kHalfStage + j * TERN_KV_BLOCK * D, vb = kb + SH::kHalfStage;
+        const float ks = sscale[s * 2 * kBlocks + j], vs = sscale[s * 2 * kBlocks + kBlocks + j];
+        // keys: tokens g and g + 8, elements t * D/4 .. of the head
+        float c[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {                            // 16 bytes of both tokens: four steps
+          const uint32_t chunk = (uint32_t)(((D == 128 ? 2 * t + h : t) ^ swz) << 4);
+          const uint4 x = lds128(kb + g * D + chunk), y = lds128(kb + (g + 8) * D + chunk);
+          const uint32_t xs[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
+          const uint32_t ys[4] = {y.x ^ 0x80808080u, y.y ^ 0x80808080u, y.z ^ 0x80808080u, y.w ^ 0x80808080u};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = codes_f16<0x4140>(xs[e]), a2 = codes_f16<0x4342>(xs[e]);
+            const uint32_t a1 = codes_f16<0x4140>(ys[e]), a3 = codes_f16<0x4342>(ys[e]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if constexpr (R == 32) {
+                const uint2 b = lds64(base + SH::kOffQ + (((4 * h + e) * NT + n) * 32 + lane) * 8);
+                mma_f16(c[n], a0, a1, a2, a3, b.x, b.y);
+              } else {
+                mma_f16(c[n], a0, a1, a2, a3, qf[n][4 * h + e][0], qf[n][4 * h + e][1]);
+              }
+            }
+          }
+        }
+        const float lv = __log2f(vs), iv = __fdividef(1.0f, vs);
+        const bool edge = t0 + TERN_KV_BLOCK > clear;
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float f0 = rowf[n][0] * ks, f1 = rowf[n][1] * ks;
+          c[n][0] = fmaf(c[n][0], f0, lv);
+          c[n][1] = fmaf(c[n][1], f1, lv);
+          c[n][2] = fmaf(c[n][2], f0, lv);
+          c[n][3] = fmaf(c[n][3], f1, lv);
+          if (edge) {
+            const int r = row0 + 8 * n + 2 * t, first = w.s.len - w.s.n;
+            const int p0 = first + r / p.group, p1 = first + (r + 1) / p.group;   // positions of the two rows
+            if (t0 + g > p0) c[n][0] = -INFINITY;
+            if (t0 + g > p1) c[n][1] = -INFINITY;
+            if (t0 + g + 8 > p0) c[n][2] = -INFINITY;
+            if (t0 + g + 8 > p1) c[n][3] = -INFINITY;
+          }
+          float x0 = fmaxf(c[n][0], c[n][2]), x1 = fmaxf(c[n][1], c[n][3]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, d));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, d));
+          }
+          const bool rise = x0 > m[n][0] + kSlack || x1 > m[n][1] + kSlack;
+          if (__any_sync(0xFFFFFFFFu, rise)) {
+            const float n0 = fmaxf(m[n][0], x0), n1 = fmaxf(m[n][1], x1);
+            const float r0 = n0 == -INFINITY ? 1.0f : exp2_approx(m[n][0] - n0), r1 = n1 == -INFINITY ? 1.0f : exp2_approx(m[n][1] - n1);
+            m[n][0] = n0;
+            m[n][1] = n1;
+            l[n][0] *= r0;
+            l[n][1] *= r1;
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+              o[k][n][0] *= r0;
+              o[k][n][1] *= r1;
+              o[k][n][2] *= r0;
+              o[k][n][3] *= r1;
+            }
+          }
+          const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+          const float e0 = exp2_approx(c[n][0] - m0), e1 = exp2_approx(c[n][1] - m1);
+          const float e2 = exp2_approx(c[n][2] - m0), e3 = exp2_approx(c[n][3] - m1);
+          l[n][0] = fmaf(e0 + e2, iv, l[n][0]);
+          l[n][1] = fmaf(e1 + e3, iv, l[n][1]);
+          pb[n][0] = movmatrix_trans(pack_f16(e0, e1));
+          pb[n][1] = movmatrix_trans(pack_f16(e2, e3));
+        }
+        // values: tokens 2t, 2t + 1, 2t + 8, 2t + 9, elements g * D/8 .. of the head
+        constexpr int W = D / 32;                                     // words of D/8 bytes
+        uint32_t v[4][W];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = 2 * t + (e & 1) + 8 * (e >> 1);
+          if constexpr (D == 128) {
+            const uint4 x = lds128(vb + tok * D + ((g ^ (tok & 7)) << 4));
+            v[e][0] = x.x; v[e][1] = x.y; v[e][2] = x.z; v[e][3] = x.w;
+          } else {
+            const uint2 x = lds64(vb + tok * D + ((((g >> 1) ^ ((tok >> 1) & 3)) << 4) | ((g & 1) << 3)));
+            v[e][0] = x.x; v[e][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const uint32_t lo0 = __byte_perm(v[0][k], v[1][k], 0x5140) ^ 0x80808080u, hi0 = __byte_perm(v[0][k], v[1][k], 0x7362) ^ 0x80808080u;
+          const uint32_t lo1 = __byte_perm(v[2][k], v[3][k], 0x5140) ^ 0x80808080u, hi1 = __byte_perm(v[2][k], v[3][k], 0x7362) ^ 0x80808080u;
+          const uint32_t a0 = codes_f16<0x4140>(lo0), a1 = codes_f16<0x4342>(lo0), a2 = codes_f16<0x4140>(lo1), a3 = codes_f16<0x4342>(lo1);
+          const uint32_t b0 = codes_f16<0x4140>(hi0), b1 = codes_f16<0x4342>(hi0), b2 = codes_f16<0x4140>(hi1), b3 = codes_f16<0x4342>(hi1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[2 * k][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            mma_f16(o[2 * k + 1][n], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * s);
+    }
+
+    // ---- join the warps: a common maximum, then the scaled sums in warp order ----
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l[n][0] += __shfl_xor_sync(0xFFFFFFFFu, l[n][0], d);
+        l[n][1] += __shfl_xor_sync(0xFFFFFFFFu, l[n][1], d);
+      }
+      if (g == 0) {
+        smax[warp * R + 8 * n + 2 * t] = m[n][0];
+        smax[warp * R + 8 * n + 2 * t + 1] = m[n][1];
+      }
+    }
+    named_sync(1, CW * 32);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float n0 = -INFINITY, n1 = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < CW; ++x) {
+        n0 = fmaxf(n0, smax[x * R + 8 * n + 2 * t]);
+        n1 = fmaxf(n1, smax[x * R + 8 * n + 2 * t + 1]);
+      }
+      const float f0 = m[n][0] == -INFINITY ? 0.0f : exp2_approx(m[n][0] - n0), f1 = m[n][1] == -INFINITY ? 0.0f : exp2_approx(m[n][1] - n1);
+      if (g == 0) {
+        ssum[warp * R + 8 * n + 2 * t] = l[n][0] * f0;
+        ssum[warp * R + 8 * n + 2 * t + 1] = l[n][1] * f1;
+      }
+      // the lane's D/8 elements of rows 2t and 2t + 1
+      float* j0 = join + (warp * R + 8 * n + 2 * t) * SH::kRowPitch + g * (D / 8);
+      float* j1 = j0 + SH::kRowPitch;
+#pragma unroll
+      for (int k = 0; k < T / 2; ++k) {
+        *reinterpret_cast<float4*>(j0 + 4 * k) = make_float4(o[2 * k][n][0] * f0, o[2 * k][n][2] * f0, o[2 * k + 1][n][0] * f0, o[2 * k + 1][n][2] * f0);
+        *reinterpret_cast<float4*>(j1 + 4 * k) = make_float4(o[2 * k][n][1] * f1, o[2 * k][n][3] * f1, o[2 * k + 1][n][1] * f1, o[2 * k + 1][n][3] * f1);
+      }
+    }
+    named_sync(1, CW * 32);
+    const long long tile0 = s0 + q0 - off, tile1 = tile0 + w.chunks;  // the tile's chunks in the whole call
+    const int c0 = (int)(tile0 / per), c1 = (int)((tile1 - 1) / per); // CTAs that share the tile
+    const bool whole = c0 == c1;
+    float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes);
+    float* part = parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * SH::kPartFloats;
+    auto write_out = [&](int r, int d, float4 v, float sum, float top) {
+      const int fr = row0 + r;
+      const int64_t at = (int64_t)(w.s.start + fr / p.group) * p.q_heads + w.hk * p.group + fr % p.group;
+      const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);      // nan stays
+      const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv), y = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(p.out + at * D + d) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      if (p.lse && d == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    };
+    for (int x = warp * 32 + lane; x < rows * (D / 4); x += CW * 32) {
+      const int r = x / (D / 4), d = x % (D / 4) * 4;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f, top = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < CW; ++y) {
+        const float4 u = *reinterpret_cast<const float4*>(join + (y * R + r) * SH::kRowPitch + d);
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        sum += ssum[y * R + r];
+        top = fmaxf(top, smax[y * R + r]);
+      }
+      if (whole) {
+        write_out(r, d, v, sum, top);
+      } else {
+        *reinterpret_cast<float4*>(part + r * D + d) = v;
+        if (d == 0) {
+          part[R * D + r] = top;
+          part[R * D + R + r] = sum;
+        }
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      named_sync(1, CW * 32);
+      int* counter = reinterpret_cast<int*>(p.ws) + c0;
+      if (threadIdx.x == 0) s_last = atomicAdd(counter, 1) == c1 - c0;
+      named_sync(1, CW * 32);
+      if (s_last) {
+        __threadfence();
+        if (threadIdx.x == 0) *counter = 0;
+        for (int x = warp * 32 + lane; x < rows * (D / 4); x += CW * 32) {
+          const int r = x / (D / 4), d = x % (D / 4) * 4;
+          float top = -INFINITY;
+          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(parts + (int64_t)(2 * c + (c == c0)) * SH::kPartFloats + R * D + r));
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float sum = 0.0f;
+          for (int c = c0; c <= c1; ++c) {
+            const float* y = parts + (int64_t)(2 * c + (c == c0)) * SH::kPartFloats;
+            const float mt = __ldcg(y + R * D + r), f = mt == -INFINITY ? 0.0f : exp2_approx(mt - top);
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(y + r * D + d));
+            v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
+            sum = fmaf(__ldcg(y + R * D + R + r), f, sum);
+          }
+          write_out(r, d, v, sum, top);
+        }
+      }
+    }
+    named_sync(1, CW * 32);                      // the join buffers are free again
+    q0 += seg;
+    off = 0;
+    if (q0 < count) w.next(p);
+  }
+  if (!ok && lane == 0) atomicExch(&g_attn_latch, 5);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }
+  return fn;
+}
+
+// The codes as rows of one token of one head; a box is one block.
+bool block_map(CUtensorMap* m, int8_t* codes, const KvView& kv, int head_dim) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)kv.pages * kv.kv_heads * kv.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)head_dim};
+  const cuuint32_t box[2] = {(cuuint32_t)head_dim, TERN_KV_BLOCK};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int R>
+cudaError_t launch_stream_t(const StreamAttn& a, bool pdl, cudaStream_t st) {
+  static std::atomic<unsigned long long> smem_raised{0};
+  cudaError_t e = allow_max_dynamic_smem(k_attn_stream<D, R>, smem_raised);
+  if (e != cudaSuccess) return e;
+  return launch_maybe_pdl(k_attn_stream<D, R>, dim3(persistent_grid(kMaxGridCTAs)), dim3(Shape<D, R>::kThreads),
+                          Shape<D, R>::kSmem, pdl, st, a);
+}
+
+template <int D>
+cudaError_t launch_stream_d(const StreamAttn& a, bool pdl, cudaStream_t st) {
+  const long long rows = (long long)a.p.max_rows * a.p.group;        // of a tile, if the caller is right
+  if (rows <= 8) return launch_stream_t<D, 8>(a, pdl, st);
+  if (rows <= 16) return launch_stream_t<D, 16>(a, pdl, st);
+  return launch_stream_t<D, 32>(a, pdl, st);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int head_dim) { return 1024; }
+size_t attn_workspace_bytes(int head_dim) {
+  return kCounterBytes + (size_t)2 * kMaxGridCTAs * (head_dim == 128 ? Shape<128, 32>::kPartFloats : Shape<64, 32>::kPartFloats) * 4;
+}
 
 cudaError_t launch_attn(const AttnParams& p, int head_dim, bool pdl, cudaStream_t st) {
-  const dim3 grid(p.kv.rows, (p.q_heads + 3) / 4);
-  return head_dim == 128 ? launch_maybe_pdl(k_attn_rows<128>, grid, dim3(128), 0, pdl, st, p)
-                         : launch_maybe_pdl(k_attn_rows<64>, grid, dim3(128), 0, pdl, st, p);
+  StreamAttn a;
+  a.p = p;
+  if (!block_map(&a.kmap, p.kv.k, p.kv, head_dim) || !block_map(&a.vmap, p.kv.v, p.kv, head_dim)) return cudaErrorInvalidValue;
+  return head_dim == 128 ? launch_stream_d<128>(a, pdl, st) : launch_stream_d<64>(a, pdl, st);
+}
+
+cudaError_t read_and_clear_attn_latch(int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_latch, sizeof(int));
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_attn_latch, &zero, sizeof(int));
 }
 
 }  // namespace tern

@@ -39,7 +39,7 @@ tern_status check_kv(const tern_kv_cache* c, const tern_kv_batch* b, int32_t* er
   if (c->pages < 1 || c->page_size < TERN_KV_BLOCK || c->page_size > 65536 || c->page_size % TERN_KV_BLOCK) return TERN_ESHAPE;
   if (!valid_heads(c->kv_heads, c->kv_heads, c->head_dim)) return TERN_ESHAPE;
   if (b->batch < 1 || b->batch > 65536 || b->rows < 0 || b->rows > kMaxRows || b->max_pages < 1 ||
-      (int64_t)b->max_pages * c->page_size > INT32_MAX)
+      (int64_t)b->max_pages * c->page_size > INT32_MAX || (int64_t)c->pages * c->kv_heads * c->page_size > INT32_MAX)
     return TERN_ESHAPE;
   if (!aligned(c->k_dev, 16) || !aligned(c->v_dev, 16) || !aligned(c->k_scale_dev, 4) || !aligned(c->v_scale_dev, 4) ||
       !aligned(b->row_start_dev, 4) || !aligned(b->kv_len_dev, 4) || !aligned(b->page_table_dev, 4) || !aligned(err_flag_dev, 4))
@@ -121,7 +121,8 @@ tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softma
   tern_status st = check_kv(cache, batch, err_flag_dev, p.kv);
   if (st != TERN_OK) return st;
   if (!q_dev || !out_dev || !workspace_dev || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
-  if (!valid_heads(q_heads, cache->kv_heads, cache->head_dim) || max_rows < 1) return TERN_ESHAPE;
+  if (!valid_heads(q_heads, cache->kv_heads, cache->head_dim) || max_rows < 1 || (int64_t)batch->rows * q_heads > INT32_MAX)
+    return TERN_ESHAPE;
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16)) return TERN_EINVAL;
   if (!std::isfinite(softmax_scale)) return TERN_EINVAL;
   if (workspace_bytes < tern::attn_workspace_bytes(cache->head_dim)) return TERN_EINVAL;

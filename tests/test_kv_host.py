@@ -54,7 +54,7 @@ def test_qkv_refusals(tg, kw, want):
 @pytest.mark.parametrize("ckw,bkw,want", [
     (dict(k_dev=None), {}, 1), (dict(v_dev=None), {}, 1), (dict(k_scale_dev=None), {}, 1), (dict(v_scale_dev=None), {}, 1),
     (dict(k_dev=FAKE + 8), {}, 1), (dict(v_dev=FAKE + 4), {}, 1), (dict(k_scale_dev=FAKE + 2), {}, 1),
-    (dict(pages=0), {}, 2), (dict(page_size=0), {}, 2), (dict(page_size=24), {}, 2), (dict(page_size=65552), {}, 2),
+    (dict(pages=0), {}, 2), (dict(pages=1 << 23), {}, 2), (dict(page_size=0), {}, 2), (dict(page_size=24), {}, 2), (dict(page_size=65552), {}, 2),
     (dict(head_dim=80), {}, 2), (dict(kv_heads=0), {}, 2), (dict(kv_heads=2000), {}, 2),
     ({}, dict(row_start_dev=None), 1), ({}, dict(kv_len_dev=None), 1), ({}, dict(page_table_dev=None), 1),
     ({}, dict(kv_len_dev=FAKE + 1), 1), ({}, dict(batch=0), 2), ({}, dict(batch=65537), 2), ({}, dict(rows=-1), 2),
