@@ -5,7 +5,7 @@
 //
 // Bound by the cache's bytes: every key and value code is read once and used for the `group`
 // query heads (times the sequence's rows) that share it. One persistent CTA per SM streams the cache
-// through a ring of shared-memory stages (TMA, one box per 16-token block, 128-byte swizzle), whatever
+// through a ring of shared-memory stages (TMA boxes of up to 64 tokens of one page, swizzled), whatever
 // sequence, head and page the tokens belong to:
 //
 //   Work.   A tile is R query rows (row x head of the group, flattened) of one sequence and one
@@ -14,7 +14,7 @@
 //           from kv_len and row_start (a captured call follows the lengths). A tile that spans CTAs
 //           leaves a partial result (max, sum, unnormalised output) per CTA in the workspace; the last
 //           CTA to arrive, by a counter, joins them in CTA order, so results do not depend on timing.
-//   Warps.  One producer warp; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
+//   Warps.  Two producer warps; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
 //           of its own (max, sum, output in registers); the warps' results are joined once per tile.
 //   Math.   S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 f16: the 16 tokens of a block are the
 //           M side of the first product, so a block's scale is one number per instruction, and the
@@ -46,6 +46,9 @@ namespace {
 
 constexpr int kChunk = 64;                        // tokens of a stage: four blocks
 constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
+// Producer warps, which take the stages in turn: issuing a stage (two boxes at about 200 cycles, a barrier
+// wait, the block scales) takes one warp 900 cycles, and the memory delivers one in 700.
+constexpr int kProducers = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum follows only when it rises by more than this (a power of two of slack in p'
 // instead of a rescale of the output for every small rise).
@@ -53,15 +56,18 @@ constexpr float kSlack = 8.0f;
 
 template <int D, int R>
 struct Shape {
-  // consumer warps; with the producer 16, 12 or 8 warps, four, three or two to a register file
+  // consumer warps; with the producers 16, 12 or 8 warps, four, three or two to a register file
   // partition: 128, 168 or 255 registers a thread
-  static constexpr int kCW = R == 8 ? 15 : R == 16 ? 11 : 7;
-  static constexpr int kThreads = (kCW + 1) * 32;
+  static constexpr int kCW = R == 8 ? 14 : R == 16 ? 10 : 6;
+  static constexpr int kThreads = (kCW + kProducers) * 32;
   static constexpr int kNT = R / 8;                               // 8-row column groups
   static constexpr int kTiles = D / 16;                           // 16-element tiles of a head
   static constexpr int kHalfStage = kChunk * D;                   // bytes of a stage's keys
-  static constexpr int kStages = (R == 32 ? 4 : 8) * 128 / D;
-  static constexpr int kRowPitch = D + 4;                         // floats of a row in the join buffer
+  static constexpr int kStages = (R == 8 ? 8 : R == 16 ? 6 : 4) * 128 / D;
+  // floats of a row in the join buffer, and where its element d sits: a lane's D/8 elements of rows 2t and
+  // 2t + 1 go out as 16-byte stores without bank conflicts
+  static constexpr int kRowPitch = D == 128 ? 148 : 84;
+  static __device__ __forceinline__ int place(int d) { return D == 128 ? d + 4 * (((d >> 4) + 1) >> 1) : d + 4 * (d >> 4); }
   // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][2][4] | masks | barriers
   static constexpr int kOffJoin = kStages * 2 * kHalfStage;
   static constexpr int kOffMax = kOffJoin + kCW * R * kRowPitch * 4;
@@ -72,8 +78,6 @@ struct Shape {
   static constexpr int kOffBar = kOffQ + (R == 32 ? D / 16 * kNT * 256 : 0);
   static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
-  // a range is at least as many chunks as give every consumer warp a block
-  static constexpr int kMinChunks = kCW / kBlocks;
 };
 constexpr int kCounterBytes = 1024;               // one counter per CTA
 
@@ -117,20 +121,20 @@ template <int R>
 struct Walk {
   SeqInfo s;
   int b, hk, qt, chunks, vis;
-  __device__ __forceinline__ static int tiles_of(const SeqInfo& s, int group) { return (s.n * group + R - 1) / R; }
+  __device__ __forceinline__ static int tiles_of(const SeqInfo& s, const FastDiv& group) { return (int)(((uint32_t)s.n * group.d + R - 1) / R); }
   // tokens that the last row of a row tile sees
-  __device__ __forceinline__ static int visible(const SeqInfo& s, int group, int qt) {
+  __device__ __forceinline__ static int visible(const SeqInfo& s, const FastDiv& group, int qt) {
     const int last = min(s.n - 1, ((qt + 1) * R - 1) / group);
     return max(0, s.len - s.n + last + 1);
   }
   __device__ __forceinline__ static int chunks_of(int vis) { return max(1, (vis + kChunk - 1) / kChunk); }
-  __device__ __forceinline__ static long long chunks_of_head(const SeqInfo& s, int group) {
+  __device__ __forceinline__ static long long chunks_of_head(const SeqInfo& s, const FastDiv& group) {
     long long sum = 0;
     const int nt = tiles_of(s, group);
     for (int q = 0; q < nt; ++q) sum += chunks_of(visible(s, group, q));
     return sum;
   }
-  __device__ __forceinline__ void set(int group) {
+  __device__ __forceinline__ void set(const FastDiv& group) {
     vis = visible(s, group, qt);
     chunks = chunks_of(vis);
   }
@@ -148,76 +152,82 @@ struct Walk {
 
 // Where a CTA's range starts.
 struct Plan {
-  long long total, per;
+  SeqInfo s;                   // of the tile's sequence
   int b, hk, qt, off;          // tile and the chunk in it
 };
 
-// Finds this CTA's range of the call's chunks. Every thread takes part.
+// Cuts the call's chunks into equal ranges and finds this CTA's: total chunks, chunks per CTA, start. Every
+// thread takes part; ends with a barrier. One load and one scan where the batch fits the block.
 template <int R, int kThreadsT>
-__device__ __forceinline__ void make_plan(const AttnParams& p, int min_chunks, Plan* plan, long long* warp_sums) {
+__device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longlong2* warp_sums, long long& total, long long& per) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWarps = kThreadsT / 32;
-  auto load = [&](int b) -> long long {
+  auto load = [&](int b, SeqInfo& s) -> long long {
+    s.n = 0;
     if (b >= p.kv.batch) return 0;
-    const SeqInfo s = seq_info(p.kv, b);
-    if (!s.ok) {
-      if (p.kv.flag && blockIdx.x == 0) *p.kv.flag = 1;
-      return 0;
-    }
-    return s.n ? Walk<R>::chunks_of_head(s, p.group) : 0;
+    s = seq_info(p.kv, b);
+    if (!s.ok && p.kv.flag && blockIdx.x == 0) *p.kv.flag = 1;
+    return s.n ? Walk<R>::chunks_of_head(s, p.group) * p.kv.kv_heads : 0;
   };
-  long long total = 0;                           // per key/value head
-  long long mine = 0;
-  for (int b = threadIdx.x; b < p.kv.batch; b += kThreadsT) mine += load(b);
+  SeqInfo s;
+  long long c = load(threadIdx.x, s), incl = c, more = 0;
+  if (p.kv.batch > kThreadsT) {
+    for (int b = threadIdx.x + kThreadsT; b < p.kv.batch; b += kThreadsT) {
+      SeqInfo x;
+      more += load(b, x);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  if (lane == 0) warp_sums[warp] = mine;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) total += warp_sums[w];
-  total *= p.kv.kv_heads;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < min_chunks) per = min_chunks;
-  const long long s0 = per * blockIdx.x;
-  if (threadIdx.x == 0) plan->total = total, plan->per = per, plan->b = -1;
-  if (s0 < total) {
-    long long base = 0;                          // chunks of the sequences before this round's
-    for (int b0 = 0; b0 < p.kv.batch; b0 += kThreadsT) {
-      const int b = b0 + threadIdx.x;
-      const long long c = load(b) * p.kv.kv_heads;
-      long long incl = c;
+    for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xFFFFFFFFu, more, o);
+  }
+  long long s0 = 0, base = 0;                    // base: chunks of the sequences before this round's
+  for (int b0 = 0; b0 < p.kv.batch; b0 += kThreadsT) {
+    if (b0) {
+      incl = c = load(b0 + threadIdx.x, s);
+      __syncthreads();
+    }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) warp_sums[warp] = incl;
-      __syncthreads();
-      long long before = base, all = base;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
-      }
-      before += incl - c;
-      if (c && s0 >= before && s0 < before + c) {
-        const SeqInfo s = seq_info(p.kv, b);
-        const long long per_head = c / p.kv.kv_heads;
-        long long rem = s0 - before;
-        plan->b = b;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sums[warp] = make_longlong2(more + incl, incl);
+    __syncthreads();
+    long long before = base + incl - c, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const longlong2 v = warp_sums[w];
+      sum += v.x;
+      base += v.y;
+      if (w < warp) before += v.y;
+    }
+    if (b0 == 0) {
+      total = sum;
+      const long long up = total + gridDim.x - 1;
+      per = up < 0x7FFFFFFFll ? (int)up / p.grid : up / gridDim.x;
+      s0 = per * blockIdx.x;
+    }
+    if (c && s0 >= before && s0 < before + c) {
+      long long rem = s0 - before;
+      const long long per_head = c / p.kv.kv_heads;
+      plan->s = s;
+      plan->b = b0 + threadIdx.x;
+      if (c < 0x7FFFFFFFll) {
+        plan->hk = (int)rem / (int)per_head;
+        rem = (int)rem % (int)per_head;
+      } else {
         plan->hk = (int)(rem / per_head);
         rem %= per_head;
-        int qt = 0;
-        for (;; ++qt) {
-          const int n = Walk<R>::chunks_of(Walk<R>::visible(s, p.group, qt));
-          if (rem < n) break;
-          rem -= n;
-        }
-        plan->qt = qt;
-        plan->off = (int)rem;
       }
-      base = all;
-      if (s0 < base) break;                      // uniform: s0 and base are
+      int qt = 0;
+      for (;; ++qt) {
+        const int n = Walk<R>::chunks_of(Walk<R>::visible(s, p.group, qt));
+        if (rem < n) break;
+        rem -= n;
+      }
+      plan->qt = qt;
+      plan->off = (int)rem;
     }
+    if (s0 < base || s0 >= total) break;         // the same for every thread
   }
   __syncthreads();
 }
@@ -236,12 +246,12 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
   uint32_t* smask = reinterpret_cast<uint32_t*>(sm + SH::kOffMask);
   const uint32_t full = base + SH::kOffBar, empty = full + 8 * ST;
   __shared__ Plan plan;
-  __shared__ long long warp_sums[SH::kThreads / 32];
+  __shared__ longlong2 warp_sums[SH::kThreads / 32];
   __shared__ int s_last;
   const AttnParams& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == CW * 32) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, kBlocks);
@@ -251,30 +261,32 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
   }
   pdl_wait();
   pdl_launch_dependents();
-  make_plan<R, SH::kThreads>(p, SH::kMinChunks, &plan, warp_sums);   // ends with a barrier
-  const long long per = plan.per, total = plan.total, s0 = per * blockIdx.x;
+  long long total, per;
+  make_plan<R, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
+  const long long s0 = per * blockIdx.x;
   if (s0 >= total) return;
   const int count = (int)min(per, total - s0);                       // chunks of this CTA
   Walk<R> w;
   w.b = plan.b;
   w.hk = plan.hk;
   w.qt = plan.qt;
-  w.s = seq_info(p.kv, w.b);
+  w.s = plan.s;
   w.set(p.group);
   int off = plan.off;
   bool ok = true;
 
-  if (warp == CW) {
-    // ---------------- producer: pages, scales and boxes, a group of 32 blocks looked up ahead ----------------
+  if (warp >= CW) {
+    // ---------------- producers: pages, scales and boxes, a group of 32 blocks looked up ahead ----------------
     struct Group {
       int row;                 // first row of the block in the tensor maps, -1: no such page, -2: past the end
       float ks, vs;
     };
+    // lane: block lane % 4 of the chunk that this warp issues lane / 4 turns after chunk0
     auto look = [&](const Walk<R>& x, int chunk0) -> Group {
       Group g{-2, 0.0f, 0.0f};
-      const int t = chunk0 * kChunk + lane * TERN_KV_BLOCK;
+      const int t = (chunk0 + lane / kBlocks * kProducers) * kChunk + lane % kBlocks * TERN_KV_BLOCK;
       if (t < x.vis) {
-        const int page = __ldg(p.kv.table + (int64_t)x.b * p.kv.max_pages + t / p.kv.page_size), place = t % p.kv.page_size;
+        const int page = __ldg(p.kv.table + (int64_t)x.b * p.kv.max_pages + t / p.page), place = t % p.page;
         g.row = -1;
         if (page >= 0 && page < p.kv.pages) {
           const int head = page * p.kv.kv_heads + x.hk;
@@ -288,45 +300,66 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
       }
       return g;
     };
-    constexpr int kAhead = 32 / kBlocks;         // chunks of a group
-    Group cur = look(w, off), nxt = cur;
-    int q = 0, at = 0;                           // ring position; chunk of the group
-    while (q < count && ok) {
-      const int seg = min(w.chunks - off, count - q);
-      for (int c = 0; c < seg; ++c, ++q) {
+    constexpr int kAhead = 32 / kBlocks;         // turns of a group
+    // blocks of a chunk that begin a box
+    const uint32_t boxes = p.box == 64 ? 1u : p.box == 32 ? 5u : 15u;
+    const int me = warp - CW;
+    int q0 = 0, last = -1;                       // ring position of the segment; of this warp's last stage
+    Group cur, nxt;
+    bool ready = false;                          // nxt is the segment's first group
+    while (q0 < count && ok) {
+      const int seg = min(w.chunks - off, count - q0);
+      const int c0 = (me + kProducers - q0 % kProducers) % kProducers;
+      if (!ready) nxt = look(w, off + c0);
+      ready = false;
+      int at = 0;
+      for (int c = c0; c < seg; c += kProducers) {
+        const int q = q0 + c, s = q % ST;
         if (at == 0) {                           // look the next group up while this one is copied
-          if (c + kAhead < seg) nxt = look(w, off + c + kAhead);
-          else if (q + seg - c < count) {
+          cur = nxt;
+          if (c + kAhead * kProducers < seg) {
+            nxt = look(w, off + c + kAhead * kProducers);
+          } else if (q0 + seg < count) {
             Walk<R> x = w;
             x.next(p);
-            nxt = look(x, 0);
+            nxt = look(x, (me + kProducers - (q0 + seg) % kProducers) % kProducers);
+            ready = true;
           }
         }
-        const int s = q % ST;
         if (q >= ST && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * s, ((q / ST) - 1) & 1)))) break;
-        const int j = lane & (kBlocks - 1), from = at * kBlocks + j;
-        const int row = __shfl_sync(0xFFFFFFFFu, cur.row, from);
-        const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, from), vs = __shfl_sync(0xFFFFFFFFu, cur.vs, from);
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, row >= 0) & ((1u << kBlocks) - 1);
-        if (lane < 2 * kBlocks) sscale[s * 2 * kBlocks + lane] = lane < kBlocks ? ks : vs;
-        if (lane == 0) smask[s] = have;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, __popc(have) * 2 * TERN_KV_BLOCK * D);
-        __syncwarp();
-        if (lane < 2 * kBlocks && row >= 0)
-          tma_load_2d(base + s * 2 * SH::kHalfStage + (lane < kBlocks ? 0 : SH::kHalfStage) + j * TERN_KV_BLOCK * D,
-                      lane < kBlocks ? &a.kmap : &a.vmap, 0, row, full + 8 * s);
-        if (++at == kAhead || c + 1 == seg) {
-          cur = nxt;
-          at = 0;
+        last = q;
+        int row[kBlocks];
+        uint32_t have = 0, bytes = 0;
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j) {
+          row[j] = __shfl_sync(0xFFFFFFFFu, cur.row, at * kBlocks + j);
+          if (row[j] >= 0) have |= 1u << j;
         }
+        // the copies first: the block's scales may still be on their way
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < kBlocks; ++j)
+            if ((boxes >> j & 1) && row[j] >= 0) {
+              const uint32_t dst = base + s * 2 * SH::kHalfStage + j * TERN_KV_BLOCK * D;
+              tma_load_2d(dst, &a.kmap, 0, row[j], full + 8 * s);
+              tma_load_2d(dst + SH::kHalfStage, &a.vmap, 0, row[j], full + 8 * s);
+              bytes += 2 * p.box * D;
+            }
+          smask[s] = have;
+        }
+        const int from = at * kBlocks + (lane & (kBlocks - 1));
+        const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, from), vs = __shfl_sync(0xFFFFFFFFu, cur.vs, from);
+        if (lane < 2 * kBlocks) sscale[s * 2 * kBlocks + lane] = lane < kBlocks ? ks : vs;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+        if (++at == kAhead) at = 0;
       }
-      if (!ok) break;
+      q0 += seg;
       off = 0;
-      if (q < count) w.next(p);
+      if (q0 < count) w.next(p);
     }
     // do not leave with copies in flight (bounded, also after a give-up)
-    for (int r = q > ST ? q - ST : 0; r < q; ++r)
+    for (int r = last; r >= 0 && r > last - ST; r -= kProducers)
       if (!mbar_wait(full + 8 * (r % ST), (r / ST) & 1)) { ok = false; break; }
     if (!ok && lane == 0) atomicExch(&g_attn_latch, 5);
     return;
@@ -338,7 +371,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
   int q0 = 0;                                                        // ring position of the segment
   while (q0 < count) {
     const int seg = min(w.chunks - off, count - q0);
-    const int rows = min(R, w.s.n * p.group - w.qt * R);             // valid rows of the tile
+    const int rows = min(R, w.s.n * (int)p.group.d - w.qt * R);      // valid rows of the tile
     const int row0 = w.qt * R;                                       // flattened: row * group + head
     // queries as fp16 fragments, each row scaled by a power of two into [2^13, 2^14)
     uint32_t qf[R == 32 ? 1 : NT][R == 32 ? 1 : T][2];
@@ -349,7 +382,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
       uint4 v[D / 32];
       float top = 0.0f;
       const bool live = 8 * n + g < rows;
-      const uint16_t* src = p.q + ((int64_t)(w.s.start + (live ? r / p.group : 0)) * p.q_heads + w.hk * p.group + (live ? r % p.group : 0)) * D + t * (D / 4);
+      const uint16_t* src = p.q + ((int64_t)(w.s.start + (live ? r / p.group : 0)) * p.q_heads + w.hk * (int)p.group.d + (live ? r % p.group : 0)) * D + t * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         v[i] = live ? ld_nc(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
@@ -389,9 +422,10 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
     if constexpr (R == 32) named_sync(1, CW * 32);
     // tokens below this are seen by every row of the tile
     const int clear = max(0, w.s.len - w.s.n + row0 / p.group + 1);
-    const int phase = (int)(((long long)q0 * kBlocks) % CW);
+    const int phase = q0 * kBlocks % CW;                             // the warp that takes the first block
+    const int turn = (warp - phase + CW) % CW, used = min(CW, seg * kBlocks);
 
-    for (int i = (warp - phase + CW) % CW; i < seg * kBlocks; i += CW) {
+    for (int i = turn; i < seg * kBlocks; i += CW) {
       const int qs = q0 + i / kBlocks, s = qs % ST, j = i % kBlocks;
       const int t0 = (off + i / kBlocks) * kChunk + j * TERN_KV_BLOCK;
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * s, (qs / ST) & 1));
@@ -529,8 +563,9 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
         ssum[warp * R + 8 * n + 2 * t] = l[n][0] * f0;
         ssum[warp * R + 8 * n + 2 * t + 1] = l[n][1] * f1;
       }
+      if (turn >= used) continue;                                     // no block was this warp's
       // the lane's D/8 elements of rows 2t and 2t + 1
-      float* j0 = join + (warp * R + 8 * n + 2 * t) * SH::kRowPitch + g * (D / 8);
+      float* j0 = join + (warp * R + 8 * n + 2 * t) * SH::kRowPitch + SH::place(g * (D / 8));
       float* j1 = j0 + SH::kRowPitch;
 #pragma unroll
       for (int k = 0; k < T / 2; ++k) {
@@ -539,14 +574,15 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
       }
     }
     named_sync(1, CW * 32);
-    const long long tile0 = s0 + q0 - off, tile1 = tile0 + w.chunks;  // the tile's chunks in the whole call
-    const int c0 = (int)(tile0 / per), c1 = (int)((tile1 - 1) / per); // CTAs that share the tile
+    // the CTAs that share the tile: it began off chunks before the segment and ends x + 1 after the range's start
+    const int x1 = q0 - off + w.chunks - 1, per32 = (int)min(per, (long long)INT32_MAX);
+    const int c0 = blockIdx.x - (off > q0 ? (off - q0 + per32 - 1) / per32 : 0), c1 = blockIdx.x + (x1 < per32 ? 0 : x1 / per32);
     const bool whole = c0 == c1;
     float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes);
     float* part = parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * SH::kPartFloats;
     auto write_out = [&](int r, int d, float4 v, float sum, float top) {
       const int fr = row0 + r;
-      const int64_t at = (int64_t)(w.s.start + fr / p.group) * p.q_heads + w.hk * p.group + fr % p.group;
+      const int64_t at = (int64_t)(w.s.start + fr / p.group) * p.q_heads + w.hk * (int)p.group.d + fr % p.group;
       const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);      // nan stays
       const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv), y = __floats2bfloat162_rn(v.z * inv, v.w * inv);
       *reinterpret_cast<uint2*>(p.out + at * D + d) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
@@ -558,8 +594,10 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
       float sum = 0.0f, top = -INFINITY;
 #pragma unroll
       for (int y = 0; y < CW; ++y) {
-        const float4 u = *reinterpret_cast<const float4*>(join + (y * R + r) * SH::kRowPitch + d);
-        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        if ((y - phase + CW) % CW < used) {
+          const float4 u = *reinterpret_cast<const float4*>(join + (y * R + r) * SH::kRowPitch + SH::place(d));
+          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
         sum += ssum[y * R + r];
         top = fmaxf(top, smax[y * R + r]);
       }
@@ -582,18 +620,30 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
       if (s_last) {
         __threadfence();
         if (threadIdx.x == 0) *counter = 0;
+        // maxima and sums of all partial results first, then their outputs, every load on its own
+        const int np = c1 - c0 + 1;
+        float* pm = join;
+        float* pl = join + np * R;
+        for (int x = warp * 32 + lane; x < np * R; x += CW * 32) {
+          const int c = c0 + x / R;
+          const float* y = parts + (int64_t)(2 * c + (c == c0)) * SH::kPartFloats + R * D + x % R;
+          const bool have = x % R < rows;
+          pm[x] = have ? __ldcg(y) : -INFINITY;
+          pl[x] = have ? __ldcg(y + R) : 0.0f;
+        }
+        named_sync(1, CW * 32);
         for (int x = warp * 32 + lane; x < rows * (D / 4); x += CW * 32) {
           const int r = x / (D / 4), d = x % (D / 4) * 4;
           float top = -INFINITY;
-          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(parts + (int64_t)(2 * c + (c == c0)) * SH::kPartFloats + R * D + r));
+          for (int i = 0; i < np; ++i) top = fmaxf(top, pm[i * R + r]);
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float sum = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* y = parts + (int64_t)(2 * c + (c == c0)) * SH::kPartFloats;
-            const float mt = __ldcg(y + R * D + r), f = mt == -INFINITY ? 0.0f : exp2_approx(mt - top);
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(y + r * D + d));
+#pragma unroll 8
+          for (int i = 0; i < np; ++i) {
+            const float mt = pm[i * R + r], f = mt == -INFINITY ? 0.0f : exp2_approx(mt - top);
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(parts + (int64_t)(2 * (c0 + i) + (i == 0)) * SH::kPartFloats + r * D + d));
             v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
-            sum = fmaf(__ldcg(y + R * D + R + r), f, sum);
+            sum = fmaf(pl[i * R + r], f, sum);
           }
           write_out(r, d, v, sum, top);
         }
@@ -619,13 +669,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// The codes as rows of one token of one head; a box is one block.
-bool block_map(CUtensorMap* m, int8_t* codes, const KvView& kv, int head_dim) {
+// The codes as rows of one token of one head; a box lies in one page.
+bool block_map(CUtensorMap* m, int8_t* codes, const KvView& kv, int head_dim, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
   if (!encode) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)kv.pages * kv.kv_heads * kv.page_size};
   const cuuint64_t strides[1] = {(cuuint64_t)head_dim};
-  const cuuint32_t box[2] = {(cuuint32_t)head_dim, TERN_KV_BLOCK};
+  const cuuint32_t box[2] = {(cuuint32_t)head_dim, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -637,13 +687,13 @@ cudaError_t launch_stream_t(const StreamAttn& a, bool pdl, cudaStream_t st) {
   static std::atomic<unsigned long long> smem_raised{0};
   cudaError_t e = allow_max_dynamic_smem(k_attn_stream<D, R>, smem_raised);
   if (e != cudaSuccess) return e;
-  return launch_maybe_pdl(k_attn_stream<D, R>, dim3(persistent_grid(kMaxGridCTAs)), dim3(Shape<D, R>::kThreads),
+  return launch_maybe_pdl(k_attn_stream<D, R>, dim3(a.p.grid.d), dim3(Shape<D, R>::kThreads),
                           Shape<D, R>::kSmem, pdl, st, a);
 }
 
 template <int D>
 cudaError_t launch_stream_d(const StreamAttn& a, bool pdl, cudaStream_t st) {
-  const long long rows = (long long)a.p.max_rows * a.p.group;        // of a tile, if the caller is right
+  const long long rows = (long long)a.p.max_rows * a.p.group.d;        // of a tile, if the caller is right
   if (rows <= 8) return launch_stream_t<D, 8>(a, pdl, st);
   if (rows <= 16) return launch_stream_t<D, 16>(a, pdl, st);
   return launch_stream_t<D, 32>(a, pdl, st);
@@ -658,7 +708,10 @@ size_t attn_workspace_bytes(int head_dim) {
 cudaError_t launch_attn(const AttnParams& p, int head_dim, bool pdl, cudaStream_t st) {
   StreamAttn a;
   a.p = p;
-  if (!block_map(&a.kmap, p.kv.k, p.kv, head_dim) || !block_map(&a.vmap, p.kv.v, p.kv, head_dim)) return cudaErrorInvalidValue;
+  a.p.grid = fast_div(persistent_grid(kMaxGridCTAs));
+  a.p.box = p.kv.page_size % 64 == 0 ? 64 : p.kv.page_size % 32 == 0 ? 32 : 16;
+  if (!block_map(&a.kmap, p.kv.k, p.kv, head_dim, a.p.box) || !block_map(&a.vmap, p.kv.v, p.kv, head_dim, a.p.box))
+    return cudaErrorInvalidValue;
   return head_dim == 128 ? launch_stream_d<128>(a, pdl, st) : launch_stream_d<64>(a, pdl, st);
 }
 

@@ -24,6 +24,24 @@ struct KvView {
   int32_t* flag;               // optional error flag
 };
 
+// Division of 0 <= n < 2^31 by a number fixed at launch: one multiply (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", PLDI 1994).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t lg = 0;
+  while ((1ull << lg) < d) ++lg;
+  // mul = floor(2^(31 + lg) / d) + 1, q = (n * mul) >> (31 + lg); d = 1: n * 2^31 / 2^31
+  return FastDiv{d, (uint32_t)((1ull << (31 + lg)) / d) + (d > 1 ? 1u : 0u), lg};
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ int operator/(int n, const FastDiv& f) {
+  return (int)(((unsigned long long)(uint32_t)n * f.mul) >> (31 + f.shift));
+}
+__device__ __forceinline__ int operator%(int n, const FastDiv& f) { return n - (n / f) * (int)f.d; }
+#endif
+
 struct QkvParams {
   const void* src;
   int64_t stride;              // elements
@@ -53,7 +71,9 @@ struct AttnParams {
   const uint16_t* q;
   uint16_t* out;
   float* lse;                  // optional
-  int32_t q_heads, group;      // group = q_heads / kv_heads
+  int32_t q_heads;
+  FastDiv group, page, grid;   // q_heads / kv_heads, page_size, CTAs of the launch
+  int32_t box;                 // tokens of a TMA box: the largest of 64, 32, 16 that divides page_size
   float scale;
   int32_t max_rows;
   uint8_t* ws;

@@ -121,7 +121,7 @@ tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softma
   tern_status st = check_kv(cache, batch, err_flag_dev, p.kv);
   if (st != TERN_OK) return st;
   if (!q_dev || !out_dev || !workspace_dev || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
-  if (!valid_heads(q_heads, cache->kv_heads, cache->head_dim) || max_rows < 1 || (int64_t)batch->rows * q_heads > INT32_MAX)
+  if (!valid_heads(q_heads, cache->kv_heads, cache->head_dim) || max_rows < 1 || (int64_t)batch->rows * q_heads > INT32_MAX - 64)
     return TERN_ESHAPE;
   if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16)) return TERN_EINVAL;
   if (!std::isfinite(softmax_scale)) return TERN_EINVAL;
@@ -131,7 +131,8 @@ tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softma
   p.out = out_dev;
   p.lse = lse_dev;
   p.q_heads = q_heads;
-  p.group = q_heads / cache->kv_heads;
+  p.group = tern::fast_div(q_heads / cache->kv_heads);
+  p.page = tern::fast_div(cache->page_size);
   p.scale = softmax_scale;
   p.max_rows = max_rows;
   p.ws = static_cast<uint8_t*>(workspace_dev);

@@ -628,7 +628,7 @@ size_t tern_paged_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_
  * out_dev bf16 [rows][q_heads][head_dim]; lse_dev optional fp32 [rows][q_heads]. A row that sees
  * nothing (kv_len < n_b) gives out = 0 and lse = -infinity.
  *   q_dev bf16 [rows][q_heads][head_dim]; q, out 16-byte aligned, not overlapping; q_heads a
- *   multiple of cache->kv_heads, at most 4096, rows * q_heads < 2^31; softmax_scale finite.
+ *   multiple of cache->kv_heads, at most 4096, rows * q_heads < 2^31 - 64; softmax_scale finite.
  *   max_rows: the largest n_b the caller expects (>= 1). It only chooses between the kernels (one that
  *   streams the cache for a few rows a sequence, one that multiplies large tiles); any value
  *   gives the right result.
