@@ -4,17 +4,18 @@
 //   s_j = scale * q.k_j,  out = sum_j e^(s_j) v_j / sum_j e^(s_j)
 //
 // Bound by the cache's bytes: every key and value code is read once and used for the `group`
-// query heads (times the sequence's rows) that share it. One persistent CTA per SM streams the cache
+// query heads (times the sequence's rows) that share it. Persistent CTAs, two on an SM for few rows, stream the cache
 // through a ring of shared-memory stages (TMA boxes of up to 64 tokens of one page, swizzled), whatever
 // sequence, head and page the tokens belong to:
 //
 //   Work.   A tile is R query rows (row x head of the group, flattened) of one sequence and one
 //           key/value head; its chunks are the 64-token stages that its last row sees. The chunks of all
-//           tiles, in order, are cut into equal contiguous ranges, one per CTA, found on the device
-//           from kv_len and row_start (a captured call follows the lengths). A tile that spans CTAs
+//           tiles, in order, each tile with a fixed cost before its chunks, are cut into equal contiguous
+//           ranges, one per CTA, found on the device from kv_len and row_start (a captured call follows
+//           the lengths). A tile that spans CTAs
 //           leaves a partial result (max, sum, unnormalised output) per CTA in the workspace; the last
 //           CTA to arrive, by a counter, joins them in CTA order, so results do not depend on timing.
-//   Warps.  Two producer warps; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
+//   Warps.  A producer warp or two; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
 //           of its own (max, sum, output in registers); the warps' results are joined once per tile.
 //   Math.   S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 f16: the 16 tokens of a block are the
 //           M side of the first product, so a block's scale is one number per instruction, and the
@@ -46,9 +47,9 @@ namespace {
 
 constexpr int kChunk = 64;                        // tokens of a stage: four blocks
 constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
-// Producer warps, which take the stages in turn: issuing a stage (two boxes at about 200 cycles, a barrier
-// wait, the block scales) takes one warp 900 cycles, and the memory delivers one in 700.
-constexpr int kProducers = 2;
+// What a tile costs beside its chunks (queries in, warps joined, result out), in chunks: measured 2.5 us of a
+// CTA that streams a chunk in 0.7 us.
+constexpr int kTileCost = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum follows only when it rises by more than this (a power of two of slack in p'
 // instead of a rescale of the output for every small rise).
@@ -56,14 +57,16 @@ constexpr float kSlack = 8.0f;
 
 template <int D, int R>
 struct Shape {
-  // consumer warps; with the producers 16, 12 or 8 warps, four, three or two to a register file
-  // partition: 128, 168 or 255 registers a thread
-  static constexpr int kCW = R == 8 ? 14 : R == 16 ? 10 : 6;
+  // CTAs on an SM: while one joins its warps at the end of a tile, the other's stream goes on. 16, 12 or 8 warps
+  // on the SM in all, four, three or two to a register file partition: 128, 168 or 255 registers a thread.
+  static constexpr int kPerSM = R == 32 ? 1 : 2;
+  static constexpr int kProducers = R == 32 ? 2 : 1;
+  static constexpr int kCW = (R == 8 ? 16 : R == 16 ? 12 : 8) / kPerSM - kProducers;   // consumer warps
   static constexpr int kThreads = (kCW + kProducers) * 32;
   static constexpr int kNT = R / 8;                               // 8-row column groups
   static constexpr int kTiles = D / 16;                           // 16-element tiles of a head
   static constexpr int kHalfStage = kChunk * D;                   // bytes of a stage's keys
-  static constexpr int kStages = (R == 8 ? 8 : R == 16 ? 6 : 4) * 128 / D;
+  static constexpr int kStages = 4 * 128 / D;
   // floats of a row in the join buffer, and where its element d sits: a lane's D/8 elements of rows 2t and
   // 2t + 1 go out as 16-byte stores without bank conflicts
   static constexpr int kRowPitch = D == 128 ? 148 : 84;
@@ -79,7 +82,8 @@ struct Shape {
   static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
 };
-constexpr int kCounterBytes = 1024;               // one counter per CTA
+constexpr int kCounterBytes = 2048;               // one counter per CTA
+static_assert(2 * kMaxGridCTAs * 4 <= kCounterBytes, "counters");
 
 struct alignas(64) StreamAttn {
   CUtensorMap kmap, vmap;      // [pages * kv_heads * page_size][head_dim] bytes, boxes of 16 rows
@@ -128,10 +132,11 @@ struct Walk {
     return max(0, s.len - s.n + last + 1);
   }
   __device__ __forceinline__ static int chunks_of(int vis) { return max(1, (vis + kChunk - 1) / kChunk); }
-  __device__ __forceinline__ static long long chunks_of_head(const SeqInfo& s, const FastDiv& group) {
+  // cost of one head's tiles
+  __device__ __forceinline__ static long long cost_of_head(const SeqInfo& s, const FastDiv& group) {
     long long sum = 0;
     const int nt = tiles_of(s, group);
-    for (int q = 0; q < nt; ++q) sum += chunks_of(visible(s, group, q));
+    for (int q = 0; q < nt; ++q) sum += chunks_of(visible(s, group, q)) + kTileCost;
     return sum;
   }
   __device__ __forceinline__ void set(const FastDiv& group) {
@@ -153,10 +158,34 @@ struct Walk {
 // Where a CTA's range starts.
 struct Plan {
   SeqInfo s;                   // of the tile's sequence
-  int b, hk, qt, off;          // tile and the chunk in it
+  int b, hk, qt, at;           // tile, and the place in its cost (kTileCost, then its chunks)
 };
 
-// Cuts the call's chunks into equal ranges and finds this CTA's: total chunks, chunks per CTA, start. Every
+// A CTA's segments: the pieces of tiles in its range, [seg chunks from chunk off of tile w].
+template <int R>
+struct Segments {
+  Walk<R> w;
+  int at, pos, count;          // place in the tile's cost; place in the range; the range's length
+  int off, seg, tile;          // tile: the tile's start, relative to the range's
+  // Moves to the next piece that has chunks; false at the end of the range.
+  __device__ __forceinline__ bool next(const AttnParams& p, bool first) {
+    for (;; first = false) {
+      if (!first) {
+        if (pos >= count) return false;
+        w.next(p);
+        at = 0;
+      }
+      tile = pos - at;
+      const int take = min(w.chunks + kTileCost - at, count - pos);
+      off = max(0, at - kTileCost);
+      seg = max(0, at + take - kTileCost) - off;
+      pos += take;
+      if (seg) return true;
+    }
+  }
+};
+
+// Cuts the call's cost into equal ranges and finds this CTA's: total cost, cost per CTA, start. Every
 // thread takes part; ends with a barrier. One load and one scan where the batch fits the block.
 template <int R, int kThreadsT>
 __device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longlong2* warp_sums, long long& total, long long& per) {
@@ -167,7 +196,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longl
     if (b >= p.kv.batch) return 0;
     s = seq_info(p.kv, b);
     if (!s.ok && p.kv.flag && blockIdx.x == 0) *p.kv.flag = 1;
-    return s.n ? Walk<R>::chunks_of_head(s, p.group) * p.kv.kv_heads : 0;
+    return s.n ? Walk<R>::cost_of_head(s, p.group) * p.kv.kv_heads : 0;
   };
   SeqInfo s;
   long long c = load(threadIdx.x, s), incl = c, more = 0;
@@ -179,7 +208,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longl
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xFFFFFFFFu, more, o);
   }
-  long long s0 = 0, base = 0;                    // base: chunks of the sequences before this round's
+  long long s0 = 0, base = 0;                    // base: cost of the sequences before this round's
   for (int b0 = 0; b0 < p.kv.batch; b0 += kThreadsT) {
     if (b0) {
       incl = c = load(b0 + threadIdx.x, s);
@@ -220,12 +249,12 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longl
       }
       int qt = 0;
       for (;; ++qt) {
-        const int n = Walk<R>::chunks_of(Walk<R>::visible(s, p.group, qt));
+        const int n = Walk<R>::chunks_of(Walk<R>::visible(s, p.group, qt)) + kTileCost;
         if (rem < n) break;
         rem -= n;
       }
       plan->qt = qt;
-      plan->off = (int)rem;
+      plan->at = (int)rem;
     }
     if (s0 < base || s0 >= total) break;         // the same for every thread
   }
@@ -233,9 +262,9 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longl
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const __grid_constant__ StreamAttn a) {
+__global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_attn_stream(const __grid_constant__ StreamAttn a) {
   using SH = Shape<D, R>;
-  constexpr int CW = SH::kCW, NT = SH::kNT, T = SH::kTiles, ST = SH::kStages;
+  constexpr int CW = SH::kCW, kProducers = SH::kProducers, NT = SH::kNT, T = SH::kTiles, ST = SH::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -265,14 +294,15 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
   make_plan<R, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
   const long long s0 = per * blockIdx.x;
   if (s0 >= total) return;
-  const int count = (int)min(per, total - s0);                       // chunks of this CTA
-  Walk<R> w;
-  w.b = plan.b;
-  w.hk = plan.hk;
-  w.qt = plan.qt;
-  w.s = plan.s;
-  w.set(p.group);
-  int off = plan.off;
+  Segments<R> sg;                                                    // the CTA's segment at hand
+  sg.w.s = plan.s;
+  sg.w.b = plan.b;
+  sg.w.hk = plan.hk;
+  sg.w.qt = plan.qt;
+  sg.w.set(p.group);
+  sg.at = plan.at;
+  sg.pos = 0;
+  sg.count = (int)min(min(per, total - s0), (long long)INT32_MAX);
   bool ok = true;
 
   if (warp >= CW) {
@@ -307,10 +337,10 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
     int q0 = 0, last = -1;                       // ring position of the segment; of this warp's last stage
     Group cur, nxt;
     bool ready = false;                          // nxt is the segment's first group
-    while (q0 < count && ok) {
-      const int seg = min(w.chunks - off, count - q0);
+    for (bool more = sg.next(p, true); more && ok; more = sg.next(p, false)) {
+      const int seg = sg.seg;
       const int c0 = (me + kProducers - q0 % kProducers) % kProducers;
-      if (!ready) nxt = look(w, off + c0);
+      if (!ready) nxt = look(sg.w, sg.off + c0);
       ready = false;
       int at = 0;
       for (int c = c0; c < seg; c += kProducers) {
@@ -318,12 +348,11 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
         if (at == 0) {                           // look the next group up while this one is copied
           cur = nxt;
           if (c + kAhead * kProducers < seg) {
-            nxt = look(w, off + c + kAhead * kProducers);
-          } else if (q0 + seg < count) {
-            Walk<R> x = w;
-            x.next(p);
-            nxt = look(x, (me + kProducers - (q0 + seg) % kProducers) % kProducers);
-            ready = true;
+            nxt = look(sg.w, sg.off + c + kAhead * kProducers);
+          } else {
+            Segments<R> x = sg;
+            ready = x.next(p, false);
+            if (ready) nxt = look(x.w, x.off + (me + kProducers - (q0 + seg) % kProducers) % kProducers);
           }
         }
         if (q >= ST && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * s, ((q / ST) - 1) & 1)))) break;
@@ -355,8 +384,6 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
         if (++at == kAhead) at = 0;
       }
       q0 += seg;
-      off = 0;
-      if (q0 < count) w.next(p);
     }
     // do not leave with copies in flight (bounded, also after a give-up)
     for (int r = last; r >= 0 && r > last - ST; r -= kProducers)
@@ -369,8 +396,9 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
   const int g = lane >> 2, t = lane & 3;
   const int swz = D == 128 ? (g & 7) : ((g >> 1) & 3);               // row g's (and g + 8's) chunk swizzle
   int q0 = 0;                                                        // ring position of the segment
-  while (q0 < count) {
-    const int seg = min(w.chunks - off, count - q0);
+  const Walk<R>& w = sg.w;
+  for (bool more = sg.next(p, true); more; more = sg.next(p, false)) {
+    const int seg = sg.seg, off = sg.off;
     const int rows = min(R, w.s.n * (int)p.group.d - w.qt * R);      // valid rows of the tile
     const int row0 = w.qt * R;                                       // flattened: row * group + head
     // queries as fp16 fragments, each row scaled by a power of two into [2^13, 2^14)
@@ -574,9 +602,9 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
       }
     }
     named_sync(1, CW * 32);
-    // the CTAs that share the tile: it began off chunks before the segment and ends x + 1 after the range's start
-    const int x1 = q0 - off + w.chunks - 1, per32 = (int)min(per, (long long)INT32_MAX);
-    const int c0 = blockIdx.x - (off > q0 ? (off - q0 + per32 - 1) / per32 : 0), c1 = blockIdx.x + (x1 < per32 ? 0 : x1 / per32);
+    // the CTAs that share the tile's chunks, the first and the last of which lie x0 and x1 after the range's start
+    const int x0 = sg.tile + kTileCost, x1 = x0 + w.chunks - 1, per32 = (int)min(per, (long long)INT32_MAX);
+    const int c0 = blockIdx.x - (x0 < 0 ? (per32 - 1 - x0) / per32 : 0), c1 = blockIdx.x + (x1 < per32 ? 0 : x1 / per32);
     const bool whole = c0 == c1;
     float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes);
     float* part = parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0)) * SH::kPartFloats;
@@ -651,8 +679,6 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, 1) k_attn_stream(const 
     }
     named_sync(1, CW * 32);                      // the join buffers are free again
     q0 += seg;
-    off = 0;
-    if (q0 < count) w.next(p);
   }
   if (!ok && lane == 0) atomicExch(&g_attn_latch, 5);
 }
@@ -683,16 +709,17 @@ bool block_map(CUtensorMap* m, int8_t* codes, const KvView& kv, int head_dim, in
 }
 
 template <int D, int R>
-cudaError_t launch_stream_t(const StreamAttn& a, bool pdl, cudaStream_t st) {
+cudaError_t launch_stream_t(StreamAttn& a, bool pdl, cudaStream_t st) {
   static std::atomic<unsigned long long> smem_raised{0};
   cudaError_t e = allow_max_dynamic_smem(k_attn_stream<D, R>, smem_raised);
   if (e != cudaSuccess) return e;
+  a.p.grid = fast_div(persistent_grid(kMaxGridCTAs) * Shape<D, R>::kPerSM);
   return launch_maybe_pdl(k_attn_stream<D, R>, dim3(a.p.grid.d), dim3(Shape<D, R>::kThreads),
                           Shape<D, R>::kSmem, pdl, st, a);
 }
 
 template <int D>
-cudaError_t launch_stream_d(const StreamAttn& a, bool pdl, cudaStream_t st) {
+cudaError_t launch_stream_d(StreamAttn& a, bool pdl, cudaStream_t st) {
   const long long rows = (long long)a.p.max_rows * a.p.group.d;        // of a tile, if the caller is right
   if (rows <= 8) return launch_stream_t<D, 8>(a, pdl, st);
   if (rows <= 16) return launch_stream_t<D, 16>(a, pdl, st);
@@ -702,13 +729,14 @@ cudaError_t launch_stream_d(const StreamAttn& a, bool pdl, cudaStream_t st) {
 }  // namespace
 
 size_t attn_workspace_bytes(int head_dim) {
-  return kCounterBytes + (size_t)2 * kMaxGridCTAs * (head_dim == 128 ? Shape<128, 32>::kPartFloats : Shape<64, 32>::kPartFloats) * 4;
+  const auto parts = [&](int rows, int per_sm) { return (size_t)2 * kMaxGridCTAs * per_sm * (rows * head_dim + 2 * rows) * 4; };
+  const size_t a = parts(32, Shape<128, 32>::kPerSM), b = parts(16, Shape<128, 16>::kPerSM);
+  return kCounterBytes + (a > b ? a : b);
 }
 
 cudaError_t launch_attn(const AttnParams& p, int head_dim, bool pdl, cudaStream_t st) {
   StreamAttn a;
   a.p = p;
-  a.p.grid = fast_div(persistent_grid(kMaxGridCTAs));
   a.p.box = p.kv.page_size % 64 == 0 ? 64 : p.kv.page_size % 32 == 0 ? 32 : 16;
   if (!block_map(&a.kmap, p.kv.k, p.kv, head_dim, a.p.box) || !block_map(&a.vmap, p.kv.v, p.kv, head_dim, a.p.box))
     return cudaErrorInvalidValue;
