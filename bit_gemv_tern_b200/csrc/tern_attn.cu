@@ -33,11 +33,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "tern_device.cuh"
+#include "tern_attn.cuh"
 #include "tern_kernels.h"
-#include "tern_kv.cuh"
-#include "tern_kv.h"
-#include "tern_mbar.cuh"
 
 namespace tern {
 
@@ -50,11 +47,6 @@ constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
 // What a tile costs beside its chunks (queries in, warps joined, result out), in chunks: measured 2.5 us of a
 // CTA that streams a chunk in 0.7 us.
 constexpr int kTileCost = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-// The running maximum follows only when it rises by more than this (a power of two of slack in p'
-// instead of a rescale of the output for every small rise).
-constexpr float kSlack = 8.0f;
-
 template <int D, int R>
 struct Shape {
   // CTAs on an SM: while one joins its warps at the end of a tile, the other's stream goes on. 16, 12 or 8 warps
@@ -82,13 +74,7 @@ struct Shape {
   static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
 };
-constexpr int kCounterBytes = 2048;               // one counter per CTA
-static_assert(2 * kMaxGridCTAs * 4 <= kCounterBytes, "counters");
 
-struct alignas(64) StreamAttn {
-  CUtensorMap kmap, vmap;      // [pages * kv_heads * page_size][head_dim] bytes, boxes of 16 rows
-  AttnParams p;
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -102,167 +88,8 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Two fp16 codes from two bytes of x, which holds code + 128: SEL 0x4140 takes bytes 0 and 1, 0x4342
-// bytes 2 and 3; 0x6400 | u is 1024 + u, and 1152 comes off again (all exact).
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
-  const uint32_t w = __byte_perm(x, 0x64646464u, SEL);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// The walk over tiles: sequence, key/value head, row tile; chunks of a tile.
-template <int R>
-struct Walk {
-  SeqInfo s;
-  int b, hk, qt, chunks, vis;
-  __device__ __forceinline__ static int tiles_of(const SeqInfo& s, const FastDiv& group) { return (int)(((uint32_t)s.n * group.d + R - 1) / R); }
-  // tokens that the last row of a row tile sees
-  __device__ __forceinline__ static int visible(const SeqInfo& s, const FastDiv& group, int qt) {
-    const int last = min(s.n - 1, ((qt + 1) * R - 1) / group);
-    return max(0, s.len - s.n + last + 1);
-  }
-  __device__ __forceinline__ static int chunks_of(int vis) { return max(1, (vis + kChunk - 1) / kChunk); }
-  // cost of one head's tiles
-  __device__ __forceinline__ static long long cost_of_head(const SeqInfo& s, const FastDiv& group) {
-    long long sum = 0;
-    const int nt = tiles_of(s, group);
-    for (int q = 0; q < nt; ++q) sum += chunks_of(visible(s, group, q)) + kTileCost;
-    return sum;
-  }
-  __device__ __forceinline__ void set(const FastDiv& group) {
-    vis = visible(s, group, qt);
-    chunks = chunks_of(vis);
-  }
-  __device__ __forceinline__ void next(const AttnParams& p) {
-    if (++qt < tiles_of(s, p.group)) return set(p.group);
-    qt = 0;
-    if (++hk < p.kv.kv_heads) return set(p.group);
-    hk = 0;
-    for (++b; b < p.kv.batch; ++b) {
-      s = seq_info(p.kv, b);
-      if (s.n) return set(p.group);
-    }
-  }
-};
-
-// Where a CTA's range starts.
-struct Plan {
-  SeqInfo s;                   // of the tile's sequence
-  int b, hk, qt, at;           // tile, and the place in its cost (kTileCost, then its chunks)
-};
-
-// A CTA's segments: the pieces of tiles in its range, [seg chunks from chunk off of tile w].
-template <int R>
-struct Segments {
-  Walk<R> w;
-  int at, pos, count;          // place in the tile's cost; place in the range; the range's length
-  int off, seg, tile;          // tile: the tile's start, relative to the range's
-  // Moves to the next piece that has chunks; false at the end of the range.
-  __device__ __forceinline__ bool next(const AttnParams& p, bool first) {
-    for (;; first = false) {
-      if (!first) {
-        if (pos >= count) return false;
-        w.next(p);
-        at = 0;
-      }
-      tile = pos - at;
-      const int take = min(w.chunks + kTileCost - at, count - pos);
-      off = max(0, at - kTileCost);
-      seg = max(0, at + take - kTileCost) - off;
-      pos += take;
-      if (seg) return true;
-    }
-  }
-};
-
-// Cuts the call's cost into equal ranges and finds this CTA's: total cost, cost per CTA, start. Every
-// thread takes part; ends with a barrier. One load and one scan where the batch fits the block.
-template <int R, int kThreadsT>
-__device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longlong2* warp_sums, long long& total, long long& per) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kWarps = kThreadsT / 32;
-  auto load = [&](int b, SeqInfo& s) -> long long {
-    s.n = 0;
-    if (b >= p.kv.batch) return 0;
-    s = seq_info(p.kv, b);
-    if (!s.ok && p.kv.flag && blockIdx.x == 0) *p.kv.flag = 1;
-    return s.n ? Walk<R>::cost_of_head(s, p.group) * p.kv.kv_heads : 0;
-  };
-  SeqInfo s;
-  long long c = load(threadIdx.x, s), incl = c, more = 0;
-  if (p.kv.batch > kThreadsT) {
-    for (int b = threadIdx.x + kThreadsT; b < p.kv.batch; b += kThreadsT) {
-      SeqInfo x;
-      more += load(b, x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xFFFFFFFFu, more, o);
-  }
-  long long s0 = 0, base = 0;                    // base: cost of the sequences before this round's
-  for (int b0 = 0; b0 < p.kv.batch; b0 += kThreadsT) {
-    if (b0) {
-      incl = c = load(b0 + threadIdx.x, s);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_sums[warp] = make_longlong2(more + incl, incl);
-    __syncthreads();
-    long long before = base + incl - c, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const longlong2 v = warp_sums[w];
-      sum += v.x;
-      base += v.y;
-      if (w < warp) before += v.y;
-    }
-    if (b0 == 0) {
-      total = sum;
-      const long long up = total + gridDim.x - 1;
-      per = up < 0x7FFFFFFFll ? (int)up / p.grid : up / gridDim.x;
-      s0 = per * blockIdx.x;
-    }
-    if (c && s0 >= before && s0 < before + c) {
-      long long rem = s0 - before;
-      const long long per_head = c / p.kv.kv_heads;
-      plan->s = s;
-      plan->b = b0 + threadIdx.x;
-      if (c < 0x7FFFFFFFll) {
-        plan->hk = (int)rem / (int)per_head;
-        rem = (int)rem % (int)per_head;
-      } else {
-        plan->hk = (int)(rem / per_head);
-        rem %= per_head;
-      }
-      int qt = 0;
-      for (;; ++qt) {
-        const int n = Walk<R>::chunks_of(Walk<R>::visible(s, p.group, qt)) + kTileCost;
-        if (rem < n) break;
-        rem -= n;
-      }
-      plan->qt = qt;
-      plan->at = (int)rem;
-    }
-    if (s0 < base || s0 >= total) break;         // the same for every thread
-  }
-  __syncthreads();
-}
-
 template <int D, int R>
-__global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_attn_stream(const __grid_constant__ StreamAttn a) {
+__global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_attn_stream(const __grid_constant__ AttnMaps a) {
   using SH = Shape<D, R>;
   constexpr int CW = SH::kCW, kProducers = SH::kProducers, NT = SH::kNT, T = SH::kTiles, ST = SH::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -291,10 +118,10 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   pdl_wait();
   pdl_launch_dependents();
   long long total, per;
-  make_plan<R, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
+  make_plan<R, kChunk, kTileCost, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
   const long long s0 = per * blockIdx.x;
   if (s0 >= total) return;
-  Segments<R> sg;                                                    // the CTA's segment at hand
+  Segments<R, kChunk, kTileCost> sg;                                                    // the CTA's segment at hand
   sg.w.s = plan.s;
   sg.w.b = plan.b;
   sg.w.hk = plan.hk;
@@ -312,7 +139,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       float ks, vs;
     };
     // lane: block lane % 4 of the chunk that this warp issues lane / 4 turns after chunk0
-    auto look = [&](const Walk<R>& x, int chunk0) -> Group {
+    auto look = [&](const auto& x, int chunk0) -> Group {
       Group g{-2, 0.0f, 0.0f};
       const int t = (chunk0 + lane / kBlocks * kProducers) * kChunk + lane % kBlocks * TERN_KV_BLOCK;
       if (t < x.vis) {
@@ -350,7 +177,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
           if (c + kAhead * kProducers < seg) {
             nxt = look(sg.w, sg.off + c + kAhead * kProducers);
           } else {
-            Segments<R> x = sg;
+            Segments<R, kChunk, kTileCost> x = sg;
             ready = x.next(p, false);
             if (ready) nxt = look(x.w, x.off + (me + kProducers - (q0 + seg) % kProducers) % kProducers);
           }
@@ -396,7 +223,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   const int g = lane >> 2, t = lane & 3;
   const int swz = D == 128 ? (g & 7) : ((g >> 1) & 3);               // row g's (and g + 8's) chunk swizzle
   int q0 = 0;                                                        // ring position of the segment
-  const Walk<R>& w = sg.w;
+  const auto& w = sg.w;
   for (bool more = sg.next(p, true); more; more = sg.next(p, false)) {
     const int seg = sg.seg, off = sg.off;
     const int rows = min(R, w.s.n * (int)p.group.d - w.qt * R);      // valid rows of the tile
@@ -421,8 +248,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       }
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      int E = (int)(__float_as_uint(top) >> 23) - 126;               // top < 2^E
-      E = max(-100, min(E, 128));
+      const int E = absmax_exponent(top);
       const float up = exp2f_i(14 - E);
       const float f = p.scale * kLog2e * exp2f_i(E - 14);
       rowf[n][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);               // rows 2t, 2t + 1 of the group of eight
@@ -709,7 +535,7 @@ bool block_map(CUtensorMap* m, int8_t* codes, const KvView& kv, int head_dim, in
 }
 
 template <int D, int R>
-cudaError_t launch_stream_t(StreamAttn& a, bool pdl, cudaStream_t st) {
+cudaError_t launch_stream_t(AttnMaps& a, bool pdl, cudaStream_t st) {
   static std::atomic<unsigned long long> smem_raised{0};
   cudaError_t e = allow_max_dynamic_smem(k_attn_stream<D, R>, smem_raised);
   if (e != cudaSuccess) return e;
@@ -719,8 +545,9 @@ cudaError_t launch_stream_t(StreamAttn& a, bool pdl, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_stream_d(StreamAttn& a, bool pdl, cudaStream_t st) {
-  const long long rows = (long long)a.p.max_rows * a.p.group.d;        // of a tile, if the caller is right
+cudaError_t launch_stream_d(AttnMaps& a, bool pdl, cudaStream_t st) {
+  const long long rows = (long long)a.p.max_rows * a.p.group.d;        // of a sequence and head, if the caller is right
+  if (rows > 32) return launch_attn_tile(a, D, pdl, st);
   if (rows <= 8) return launch_stream_t<D, 8>(a, pdl, st);
   if (rows <= 16) return launch_stream_t<D, 16>(a, pdl, st);
   return launch_stream_t<D, 32>(a, pdl, st);
@@ -731,11 +558,12 @@ cudaError_t launch_stream_d(StreamAttn& a, bool pdl, cudaStream_t st) {
 size_t attn_workspace_bytes(int head_dim) {
   const auto parts = [&](int rows, int per_sm) { return (size_t)2 * kMaxGridCTAs * per_sm * (rows * head_dim + 2 * rows) * 4; };
   const size_t a = parts(32, Shape<128, 32>::kPerSM), b = parts(16, Shape<128, 16>::kPerSM);
-  return kCounterBytes + (a > b ? a : b);
+  const size_t c = kCounterBytes + (a > b ? a : b), t = attn_tile_workspace_bytes(head_dim);
+  return c > t ? c : t;
 }
 
 cudaError_t launch_attn(const AttnParams& p, int head_dim, bool pdl, cudaStream_t st) {
-  StreamAttn a;
+  AttnMaps a;
   a.p = p;
   a.p.box = p.kv.page_size % 64 == 0 ? 64 : p.kv.page_size % 32 == 0 ? 32 : 16;
   if (!block_map(&a.kmap, p.kv.k, p.kv, head_dim, a.p.box) || !block_map(&a.vmap, p.kv.v, p.kv, head_dim, a.p.box))

@@ -81,6 +81,7 @@ struct AttnParams {
 size_t attn_workspace_bytes(int head_dim);
 cudaError_t launch_attn(const AttnParams& p, int head_dim, bool pdl, cudaStream_t st);
 cudaError_t read_and_clear_attn_latch(int* out);
+cudaError_t read_and_clear_attn_tile_latch(int* out);
 
 // One launch, optionally with programmatic stream serialisation (the kernel calls pdl_wait()).
 template <typename P>
