@@ -101,22 +101,28 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t saddr) {
   d |= (uint64_t)2u << 61;
   return d;
 }
+// The tensor-core instructions below are reached by a whole warp with the same operands, so that those stay in uniform
+// registers, and issued by one elected lane.
 // D[tmem] (+)= A[smem] B[smem], fp16 operands, fp32 accumulator.
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem].
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       for (int r = n > 2 ? n - 2 : 0; r < n; ++r)
         if (!mbar_wait(raw_full + 8 * (r & 1), (r >> 1) & 1)) { ok = false; break; }
     } else if (warp == 13) {
-      // ---------------- MMA issue (lane 0) ----------------
+      // ---------------- MMA issue ----------------
       int n = 0;                                                     // chunks begun
       int nq0 = 0, nq1 = 0, tiles0 = 0, tiles1 = 0;                  // chunks, tiles of each half
       const uint64_t dQ = umma_desc(sQ), dK = umma_desc(sK), dV = umma_desc(sV);     // + offset / 16: the address field
@@ -397,13 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
         if (!g) break;
         const int halves = g->rows > kHalf ? 2 : 1, seg = g->seg;
         give(turn);
-        if (lane == 0) [&] {
-        if (!(ok = mbar_wait(k_full + 8 * (n & 1), (n >> 1) & 1))) return;
+        [&] {
+        if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(k_full + 8 * (n & 1), (n >> 1) & 1)))) return;
 #pragma unroll 1
         for (int q = 0; q < halves; ++q) {
           // the half's queries are in, and the last tile's P (where S goes) has been multiplied
           const int nq = q ? nq1 : nq0;
-          ok = mbar_wait(q_full + 8 * q, (q ? tiles1 : tiles0) & 1) && (nq == 0 || mbar_wait(pv_done + 8 * q, (nq - 1) & 1));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_full + 8 * q, (q ? tiles1 : tiles0) & 1) &&
+                                           (nq == 0 || mbar_wait(pv_done + 8 * q, (nq - 1) & 1)));
           if (!ok) return;
           ++(q ? tiles1 : tiles0);
           tc_fence_after();
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
 #pragma unroll 1
           for (int q = 0; q < halves; ++q) {
             const int nq = q ? nq1++ : nq0++;
-            ok = mbar_wait(p_full + 8 * q, nq & 1) && (q || mbar_wait(v_full, n & 1));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(p_full + 8 * q, nq & 1) && (q || mbar_wait(v_full, n & 1)));
             if (!ok) return;
             tc_fence_after();
 #pragma unroll
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
             if (c + 1 < seg) {
               const int buf = (n + 1) & 1;
               // P may be overwritten by the next scores only once it has been read
-              ok = (q || mbar_wait(k_full + 8 * buf, ((n + 1) >> 1) & 1)) && mbar_wait(pv_done + 8 * q, nq & 1);
+              ok = __all_sync(0xFFFFFFFFu, (q || mbar_wait(k_full + 8 * buf, ((n + 1) >> 1) & 1)) && mbar_wait(pv_done + 8 * q, nq & 1));
               if (!ok) return;
               scores(q, buf);
               if (q == halves - 1) umma_commit(k_empty + 8 * buf);
@@ -434,13 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           }
         }
         }();
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       }
-      // every MMA this thread issued has completed once done_bar flips
-      if (lane == 0) {
-        umma_commit(done_bar);
-        if (!mbar_wait(done_bar, 0)) ok = false;
-      }
+      // every MMA issued has completed once done_bar flips
+      umma_commit(done_bar);
+      if (!mbar_wait(done_bar, 0)) ok = false;
     } else if (warp == 14) {
       // ---------------- the walk ----------------
       Segments<kRows, kChunk, kTileCost> sg;
