@@ -45,12 +45,13 @@ constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
 // What a tile costs beside its chunks (queries in, results out), in chunks of about a microsecond.
 constexpr int kTileCost = 2;
 constexpr int kThreads = 512;
+constexpr uint32_t kIdlePolls = 1u << 25;          // polls without progress (seconds) before the MMA warp gives up
 constexpr int kDecWarps = 4;
 constexpr int kPanel = 128 * 128;                 // a swizzled panel of 128 rows x 64 fp16
 // block scales of this many chunks: values lag keys by one chunk and the ring of codes is two, so three are in use
 constexpr int kScaleSlots = 4;
 // registers a thread of the softmax warpgroups and of the others: they add up to what the launch has
-constexpr int kRegsSoftmax = 168, kRegsOther = 88;
+constexpr int kRegsSoftmax = 192, kRegsOther = 64;
 static_assert((kRegsSoftmax + kRegsOther) * (kThreads / 2) == 128 * kThreads, "register split");
 
 // A piece of a tile: what the warps need to know of it.
@@ -76,7 +77,7 @@ struct Tile {
   static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffRaw = kOffV + kV;
   static constexpr int kOffScale = kOffRaw + 2 * 2 * kRaw;          // [slot][ks, log2 vs, 1 / vs][block]
   static constexpr int kOffBar = kOffScale + kScaleSlots * 3 * kBlocks * 4;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 2 + 1 + 2 * kSegments;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 2 + 1 + 2 * kSegments;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kPartFloats = kHalf * D + 2 * kHalf;         // a half's partial result
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kChunk >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
@@ -234,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
   uint8_t* sm = smem_raw + (base - raw0);
   float* sscale = reinterpret_cast<float*>(sm + SH::kOffScale);
   const uint32_t sQ = base, sK = base + SH::kOffK, sV = base + SH::kOffV, sRaw = base + SH::kOffRaw;
-  const uint32_t raw_full = base + SH::kOffBar, raw_empty = raw_full + 16, k_full = raw_empty + 16, k_empty = k_full + 16;
+  const uint32_t kr_full = base + SH::kOffBar, kr_empty = kr_full + 16, vr_full = kr_empty + 16, vr_empty = vr_full + 16;
+  const uint32_t k_full = vr_empty + 16, k_empty = k_full + 16;
   const uint32_t v_full = k_empty + 16, v_empty = v_full + 8, q_full = v_empty + 8, s_full = q_full + 16, p_full = s_full + 16;
   const uint32_t pv_done = p_full + 16, done_bar = pv_done + 16;
   const uint32_t seg_full = done_bar + 8, seg_empty = seg_full + 8 * kSegments, tmem_slot = seg_empty + 8 * kSegments;
@@ -246,8 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
 
   if (threadIdx.x == 12 * 32) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(raw_full + 8 * i, 1);
-      mbar_init(raw_empty + 8 * i, kDecWarps);
+      mbar_init(kr_full + 8 * i, 1);
+      mbar_init(kr_empty + 8 * i, kDecWarps);
+      mbar_init(vr_full + 8 * i, 1);
+      mbar_init(vr_empty + 8 * i, kDecWarps);
       mbar_init(k_full + 8 * i, kDecWarps);
       mbar_init(k_empty + 8 * i, 1);
       mbar_init(q_full + 8 * i, 4);
@@ -297,14 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       // ---------------- codes to operand tiles: the next chunk's keys before this one's values ----------------
       const int wd = warp - 8;
       auto values = [&](int i) {                                     // of chunk i
-        ok = __all_sync(0xFFFFFFFFu, i < 1 || mbar_wait(v_empty, (i - 1) & 1));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(vr_full + 8 * (i & 1), (i >> 1) & 1) && (i < 1 || mbar_wait(v_empty, (i - 1) & 1)));
         if (!ok) return;
-        expand_values<D>(sRaw + (i & 1) * 2 * SH::kRaw + SH::kRaw, sV, wd, lane);
+        expand_values<D>(sRaw + (2 + (i & 1)) * SH::kRaw, sV, wd, lane);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(v_full);
-          mbar_arrive(raw_empty + 8 * (i & 1));
+          mbar_arrive(vr_empty + 8 * (i & 1));
         }
       };
       int i = 0;                                                     // chunk
@@ -315,20 +319,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
         give(turn);
         for (; i < end && ok; ++i) {
           const int s = i & 1;
-          ok = mbar_wait(raw_full + 8 * s, (i >> 1) & 1) && (i < 2 || mbar_wait(k_empty + 8 * s, ((i >> 1) - 1) & 1));
+          ok = mbar_wait(kr_full + 8 * s, (i >> 1) & 1) && (i < 2 || mbar_wait(k_empty + 8 * s, ((i >> 1) - 1) & 1));
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-          expand_keys<D>(sRaw + s * 2 * SH::kRaw, sK + s * SH::kK, wd, lane);
+          expand_keys<D>(sRaw + s * SH::kRaw, sK + s * SH::kK, wd, lane);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(k_full + 8 * s);
+          if (lane == 0) {
+            mbar_arrive(k_full + 8 * s);
+            mbar_arrive(kr_empty + 8 * s);
+          }
           if (i > 0) values(i - 1);
         }
       }
       if (ok && i > 0) values(i - 1);
     } else if (warp == 12) {
       // ---------------- producer ----------------
-      int n = 0;                                                     // chunks issued
+      int n = 0, nk = 0;                                             // chunks issued: values, keys
       for (int turn = 0; ok; ++turn) {
         const Segment* g = take(turn, ok);
         if (!g) break;
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
             }
           }
           const int s = n & 1, slot = n % kScaleSlots;
-          if (n >= 2 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw_empty + 8 * s, ((n >> 1) - 1) & 1)))) break;
+          if (n >= 2 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(kr_empty + 8 * s, ((n >> 1) - 1) & 1)))) break;
           // blocks 0..7 of the chunk to lanes 0..7
           const int src = 8 * at + (lane & 7);
           const int r = __shfl_sync(0xFFFFFFFFu, row, src);
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           const int step = p.box / TERN_KV_BLOCK;
           const bool copies = lane < kBlocks && r >= 0 && (lane & (step - 1)) == 0;
           const uint32_t have = __ballot_sync(0xFFFFFFFFu, copies);
-          // the scales, ordered before the scores by raw_full, k_full and s_full; a block that is not there gets
+          // the scales, ordered before the scores by kr_full, k_full and s_full; a block that is not there gets
           // scores of 0 * anything - infinity
           if (lane < kBlocks) {
             float* sc = sscale + slot * 3 * kBlocks + lane;
@@ -374,18 +381,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
             sc[2 * kBlocks] = r >= 0 ? __fdividef(1.0f, v) : 0.0f;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(raw_full + 8 * s, __popc(have) * 2 * p.box * D);
+          const uint32_t bytes = __popc(have) * p.box * D, dst = sRaw + s * SH::kRaw + lane * TERN_KV_BLOCK * D;
+          if (lane == 0) mbar_arrive_expect_tx(kr_full + 8 * s, bytes);
           __syncwarp();
-          if (copies) {
-            const uint32_t dst = sRaw + s * 2 * SH::kRaw + lane * TERN_KV_BLOCK * D;
-            tma_load_2d(dst, &a.kmap, 0, r, raw_full + 8 * s);
-            tma_load_2d(dst + SH::kRaw, &a.vmap, 0, r, raw_full + 8 * s);
+          if (copies) tma_load_2d(dst, &a.kmap, 0, r, kr_full + 8 * s);
+          if (n >= 2 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(vr_empty + 8 * s, ((n >> 1) - 1) & 1)))) {
+            ++nk;
+            break;
           }
+          if (lane == 0) mbar_arrive_expect_tx(vr_full + 8 * s, bytes);
+          __syncwarp();
+          if (copies) tma_load_2d(dst + 2 * SH::kRaw, &a.vmap, 0, r, vr_full + 8 * s);
+          ++nk;
         }
       }
       // do not leave with copies in flight (bounded, also after a give-up)
-      for (int r = n > 2 ? n - 2 : 0; r < n; ++r)
-        if (!mbar_wait(raw_full + 8 * (r & 1), (r >> 1) & 1)) { ok = false; break; }
+      for (int r = nk > 2 ? nk - 2 : 0; r < nk; ++r)
+        if (!mbar_wait(kr_full + 8 * (r & 1), (r >> 1) & 1) || (r < n && !mbar_wait(vr_full + 8 * (r & 1), (r >> 1) & 1))) { ok = false; break; }
     } else if (warp == 13) {
       // ---------------- MMA issue ----------------
       int n = 0;                                                     // chunks begun
@@ -417,29 +429,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           scores(q, n & 1);
         }
         umma_commit(k_empty + 8 * (n & 1));
-        for (int c = 0; c < seg; ++c, ++n) {
+        // Whichever half is ready goes next: O += P V once its probabilities are there, then, once that has read P
+        // (the next scores go over it), the next chunk's scores.
+        int c0 = 0, c1 = halves == 2 ? 0 : seg;                      // chunk of each half
+        bool w0 = false, w1 = false;                                 // waiting for its product
+        int vs = 0, ks = 0;                                          // halves done with the values, the next keys
+        uint32_t idle = 0;
+        while (c0 < seg || c1 < seg) {
+          bool moved = false;
 #pragma unroll 1
-          for (int q = 0; q < halves; ++q) {
-            const int nq = q ? nq1++ : nq0++;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(p_full + 8 * q, nq & 1) && (q || mbar_wait(v_full, n & 1)));
-            if (!ok) return;
-            tc_fence_after();
+          for (int q = 0; q < 2; ++q) {
+            const int c = q ? c1 : c0, nq = q ? nq1 : nq0;
+            if (c >= seg) continue;
+            if (!(q ? w1 : w0)) {
+              if (!mbar_test(p_full + 8 * q, nq & 1) || !mbar_test(v_full, (n + c) & 1)) continue;
+              tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kChunk / 16; ++k)
-              umma_ts(tmem + 2 * kChunk + q * D, tmem + q * kChunk + 8 * k, dV + (uint32_t)(((k >> 2) * SH::kVPanel + 32 * (k & 3)) >> 4),
-                      SH::kIdescO, c > 0 || k > 0);
-            umma_commit(pv_done + 8 * q);
-            if (q == halves - 1) umma_commit(v_empty);
-            if (c + 1 < seg) {
-              const int buf = (n + 1) & 1;
-              // P may be overwritten by the next scores only once it has been read
-              ok = __all_sync(0xFFFFFFFFu, (q || mbar_wait(k_full + 8 * buf, ((n + 1) >> 1) & 1)) && mbar_wait(pv_done + 8 * q, nq & 1));
-              if (!ok) return;
+              for (int k = 0; k < kChunk / 16; ++k)
+                umma_ts(tmem + 2 * kChunk + q * D, tmem + q * kChunk + 8 * k, dV + (uint32_t)(((k >> 2) * SH::kVPanel + 32 * (k & 3)) >> 4),
+                        SH::kIdescO, c > 0 || k > 0);
+              umma_commit(pv_done + 8 * q);
+              if (++vs == halves) {
+                umma_commit(v_empty);
+                vs = 0;
+              }
+              if (c + 1 < seg) (q ? w1 : w0) = true;
+              else { ++(q ? c1 : c0); ++(q ? nq1 : nq0); }
+            } else {
+              const int buf = (n + c + 1) & 1;
+              if (!mbar_test(pv_done + 8 * q, nq & 1) || !mbar_test(k_full + 8 * buf, ((n + c + 1) >> 1) & 1)) continue;
+              tc_fence_after();
               scores(q, buf);
-              if (q == halves - 1) umma_commit(k_empty + 8 * buf);
+              if (++ks == halves) {
+                umma_commit(k_empty + 8 * buf);
+                ks = 0;
+              }
+              (q ? w1 : w0) = false;
+              ++(q ? c1 : c0);
+              ++(q ? nq1 : nq0);
             }
+            moved = true;
+          }
+          idle = moved ? 0 : idle + 1;
+          if (idle > kIdlePolls) {
+            ok = false;
+            return;
           }
         }
+        n += seg;
         }();
       }
       // every MMA issued has completed once done_bar flips
@@ -550,36 +587,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           cf[j] = pack2(rowf * ks.x, rowf * ks.y);
           lv[j] = pack2(x.x, x.y);
         }
-        // S is read twice, 32 columns at a time, instead of held
-        const bool edge = t0 + kChunk > clear;
-        const int lim = pos - t0;                                    // the last visible token of the chunk
-        uint32_t s[2][32];
-        tmem_ld32(tS, s[0]);
-        // the exponents of columns 2 i, 2 i + 1 of the piece h; masked where the chunk reaches past a row's position
-        auto pair = [&](int h, int i, bool masked, float& x, float& y) {
-          unpack2(fma2(pack2(__uint_as_float(s[h & 1][2 * i]), __uint_as_float(s[h & 1][2 * i + 1])), cf[i & 3], lv[i & 3]), x, y);
-          if (masked) {
-            const int row = 32 * h + 2 * i, tok = 16 * (row & 7) + (row >> 3);
-            x = tok > lim ? -INFINITY : x;
-            y = tok + 16 > lim ? -INFINITY : y;
-          }
-        };
+        uint32_t s[kChunk];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
+        tmem_wait_ld();
+        // the exponents (base 2) of the row's probabilities; pairs of columns, whose blocks repeat every eight columns
+        uint64_t t[kChunk / 2];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto maxima = [&](bool masked) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            tmem_wait_ld();
-            tmem_ld32(tS + 32 * ((h + 1) & 3), s[(h + 1) & 1]);      // at the end the first ones again
+        for (int i = 0; i < kChunk / 2; ++i)
+          t[i] = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cf[i & 3], lv[i & 3]);
+        if (t0 + kChunk > clear) {
+          const int lim = pos - t0;                                  // the last visible token of the chunk
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x, y;
-              pair(h, i, masked, x, y);
-              asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(x), "f"(y));
-            }
+          for (int i = 0; i < kChunk / 2; ++i) {
+            float x, y;
+            unpack2(t[i], x, y);
+            const int row = 2 * i, tok = 16 * (row & 7) + (row >> 3);
+            t[i] = pack2(tok > lim ? -INFINITY : x, tok + 16 > lim ? -INFINITY : y);
           }
-        };
-        if (edge) maxima(true);
-        else maxima(false);
+        }
+#pragma unroll
+        for (int i = 0; i < kChunk / 2; ++i) {
+          float x, y;
+          unpack2(t[i], x, y);
+          asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(x), "f"(y));
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
           const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
@@ -601,30 +634,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
         const uint64_t neg2 = pack2(neg, neg);
         uint64_t acc[kBlocks / 2];
 #pragma unroll
-        for (int j = 0; j < kBlocks / 2; ++j) {
-          lv[j] = add2(lv[j], neg2);
-          acc[j] = 0;
-        }
-        auto probabilities = [&](bool masked) {
+        for (int j = 0; j < kBlocks / 2; ++j) acc[j] = 0;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            tmem_wait_ld();
-            if (h < 3) tmem_ld32(tS + 32 * (h + 1), s[(h + 1) & 1]);
-            uint32_t pk[16];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x, y;
-              pair(h, i, masked, x, y);
-              x = exp2_approx(x);
-              y = exp2_approx(y);
-              acc[i & 3] = add2(acc[i & 3], pack2(x, y));
-              pk[i] = pack_f16(x, y);
-            }
-            tmem_st16(tS + 16 * h, pk);                              // over columns 16 h .. of S, which have been read
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack2(add2(t[16 * h + i], neg2), x, y);
+            x = exp2_approx(x);
+            y = exp2_approx(y);
+            acc[i & 3] = add2(acc[i & 3], pack2(x, y));
+            pk[i] = pack_f16(x, y);
           }
-        };
-        if (edge) probabilities(true);
-        else probabilities(false);
+          tmem_st16(tS + 16 * h, pk);
+        }
 #pragma unroll
         for (int j = 0; j < kBlocks / 2; ++j) {
           float x, y;
