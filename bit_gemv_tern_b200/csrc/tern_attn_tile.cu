@@ -13,9 +13,10 @@
 //               [element][token], both K-major with 128-byte swizzle;
 //   warp 12     TMA of the raw codes (boxes of up to 64 tokens of a page), block scales;
 //   warp 14     walks the CTA's range and hands the other warps their segments through a ring;
-//   warp 13     one thread issues tcgen05.mma kind::f16: S = Q K^T (A = Q and B = K from shared
-//               memory), O += P V (A = P from TMEM, B = V^T). While one half's softmax runs, the other
-//               half's products do.
+//   warps 13, 15  issue the tcgen05.mma kind::f16 of a half each: S = Q K^T (A = Q and B = K from shared
+//               memory), O += P V (A = P from TMEM, B = V^T), in steps of 64 of a chunk's tokens: while
+//               the softmax works on one step's scores, the other step is multiplied and its next
+//               scores are made.
 // TMEM: S of the two halves (128 columns each, P over them), O of the two halves (128 each): all 512.
 // Token order: the key tile's row 8 o + j holds token 16 j + o of the chunk, so that the transposition of the
 // values reads and writes shared memory without bank conflicts; column r of S is then of block r % 8, and the
@@ -42,16 +43,16 @@ namespace {
 constexpr int kRows = 256, kHalf = 128;           // rows of a tile, of an MMA
 constexpr int kChunk = 128;                       // tokens of a chunk
 constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
+constexpr int kSub = 64;                          // columns of S that a softmax step and a pair of products take
 // What a tile costs beside its chunks (queries in, results out), in chunks of about a microsecond.
 constexpr int kTileCost = 2;
 constexpr int kThreads = 512;
-constexpr uint32_t kIdlePolls = 1u << 25;          // polls without progress (seconds) before the MMA warp gives up
 constexpr int kDecWarps = 4;
 constexpr int kPanel = 128 * 128;                 // a swizzled panel of 128 rows x 64 fp16
 // block scales of this many chunks: values lag keys by one chunk and the ring of codes is two, so three are in use
 constexpr int kScaleSlots = 4;
 // registers a thread of the softmax warpgroups and of the others: they add up to what the launch has
-constexpr int kRegsSoftmax = 192, kRegsOther = 64;
+constexpr int kRegsSoftmax = 144, kRegsOther = 112;
 static_assert((kRegsSoftmax + kRegsOther) * (kThreads / 2) == 128 * kThreads, "register split");
 
 // A piece of a tile: what the warps need to know of it.
@@ -64,7 +65,7 @@ struct Segment {
   int pad;
 };
 constexpr int kSegments = 4;                      // ring of segments
-constexpr int kSegWarps = 8 + kDecWarps + 2;      // warps that read it
+constexpr int kSegWarps = 8 + kDecWarps + 3;      // warps that read it
 
 template <int D>
 struct Tile {
@@ -77,10 +78,10 @@ struct Tile {
   static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffRaw = kOffV + kV;
   static constexpr int kOffScale = kOffRaw + 2 * 2 * kRaw;          // [slot][ks, log2 vs, 1 / vs][block]
   static constexpr int kOffBar = kOffScale + kScaleSlots * 3 * kBlocks * 4;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 2 + 1 + 2 * kSegments;
+  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 4 + 4 + 4 + 2 + 2 * kSegments;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kPartFloats = kHalf * D + 2 * kHalf;         // a half's partial result
-  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kChunk >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
+  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kSub >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
 };
 
@@ -102,28 +103,29 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t saddr) {
   d |= (uint64_t)2u << 61;
   return d;
 }
-// The tensor-core instructions below are reached by a whole warp with the same operands, so that those stay in uniform
-// registers, and issued by one elected lane.
+// One lane of the (converged) warp, chosen so that the compiler keeps the tensor-core operands of the code it guards in
+// uniform registers: three instructions an MMA, against twelve behind a test of threadIdx.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
 // D[tmem] (+)= A[smem] B[smem], fp16 operands, fp32 accumulator.
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem].
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xFFFFFFFF;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar) : "memory");
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -169,6 +171,11 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -237,9 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
   const uint32_t sQ = base, sK = base + SH::kOffK, sV = base + SH::kOffV, sRaw = base + SH::kOffRaw;
   const uint32_t kr_full = base + SH::kOffBar, kr_empty = kr_full + 16, vr_full = kr_empty + 16, vr_empty = vr_full + 16;
   const uint32_t k_full = vr_empty + 16, k_empty = k_full + 16;
-  const uint32_t v_full = k_empty + 16, v_empty = v_full + 8, q_full = v_empty + 8, s_full = q_full + 16, p_full = s_full + 16;
-  const uint32_t pv_done = p_full + 16, done_bar = pv_done + 16;
-  const uint32_t seg_full = done_bar + 8, seg_empty = seg_full + 8 * kSegments, tmem_slot = seg_empty + 8 * kSegments;
+  const uint32_t v_full = k_empty + 16, v_empty = v_full + 8, q_full = v_empty + 8;
+  const uint32_t s_full = q_full + 16, p_full = s_full + 32;       // [half][step]
+  const uint32_t pv_done = p_full + 32, done_bar = pv_done + 32;
+  const uint32_t seg_full = done_bar + 16, seg_empty = seg_full + 8 * kSegments, tmem_slot = seg_empty + 8 * kSegments;
   __shared__ Plan plan;
   __shared__ longlong2 warp_sums[kThreads / 32];
   __shared__ Segment segs[kSegments];
@@ -253,19 +261,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       mbar_init(vr_full + 8 * i, 1);
       mbar_init(vr_empty + 8 * i, kDecWarps);
       mbar_init(k_full + 8 * i, kDecWarps);
-      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 2);
       mbar_init(q_full + 8 * i, 4);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
       mbar_init(pv_done + 8 * i, 1);
     }
     mbar_init(v_full, kDecWarps);
-    mbar_init(v_empty, 1);
+    mbar_init(v_empty, 2);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(seg_full + 8 * i, 1);
       mbar_init(seg_empty + 8 * i, kSegWarps);
     }
     mbar_init(done_bar, 1);
+    mbar_init(done_bar + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -398,90 +409,84 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       // do not leave with copies in flight (bounded, also after a give-up)
       for (int r = nk > 2 ? nk - 2 : 0; r < nk; ++r)
         if (!mbar_wait(kr_full + 8 * (r & 1), (r >> 1) & 1) || (r < n && !mbar_wait(vr_full + 8 * (r & 1), (r >> 1) & 1))) { ok = false; break; }
-    } else if (warp == 13) {
-      // ---------------- MMA issue ----------------
-      int n = 0;                                                     // chunks begun
-      int nq0 = 0, nq1 = 0, tiles0 = 0, tiles1 = 0;                  // chunks, tiles of each half
+    } else if (warp == 13 || warp == 15) {
+      // ---------------- MMA issue, a warp for each half ----------------
       const uint64_t dQ = umma_desc(sQ), dK = umma_desc(sK), dV = umma_desc(sV);     // + offset / 16: the address field
-      auto scores = [&](int q, int buf) {
+      const int q = warp == 15;
+      const uint32_t tS = tmem + q * kChunk, tO = tmem + 2 * kChunk + q * D;
+      // the scores of step x (64 of the chunk's tokens) from key buffer `buf`; last: the buffer is done with
+      auto scores = [&](int x, int buf, bool last) {
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = dQ + (uint32_t)(q * (SH::kQ >> 4)), b = dK + (uint32_t)(buf * (SH::kK >> 4) + x * (kSub * 128 >> 4));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_ss(tmem + q * kChunk, dQ + (uint32_t)((q * SH::kQ + (k >> 2) * kPanel + 32 * (k & 3)) >> 4),
-                  dK + (uint32_t)((buf * SH::kK + (k >> 2) * kPanel + 32 * (k & 3)) >> 4), SH::kIdescS, k > 0);
-        umma_commit(s_full + 8 * q);
+          for (int k = 0; k < D / 16; ++k)
+            umma_ss(tS + x * kSub, a + (uint32_t)(((k >> 2) * kPanel + 32 * (k & 3)) >> 4),
+                    b + (uint32_t)(((k >> 2) * kPanel + 32 * (k & 3)) >> 4), SH::kIdescS, k > 0);
+          umma_commit(s_full + 8 * (2 * q + x));
+          if (last) umma_commit(k_empty + 8 * buf);
+        }
+        __syncwarp();
       };
+      // O += P V of step x; more: O holds earlier products
+      auto product = [&](int x, bool more) {
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t b = dV + (uint32_t)(x * (SH::kVPanel >> 4));
+#pragma unroll
+          for (int k = 0; k < kSub / 16; ++k)
+            umma_ts(tO, tS + x * kSub + 8 * k, b + (uint32_t)(32 * k >> 4), SH::kIdescO, k > 0 ? 1u : (uint32_t)more);
+          umma_commit(pv_done + 8 * (2 * q + x));
+          if (x) umma_commit(v_empty);
+        }
+        __syncwarp();
+      };
+      auto wait = [&](uint32_t bar, int phase) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1));
+        return ok;
+      };
+      int n = 0, nq = 0, tiles = 0;                                  // chunks begun; chunks, tiles of this half
       for (int turn = 0; ok; ++turn) {
         const Segment* g = take(turn, ok);
         if (!g) break;
-        const int halves = g->rows > kHalf ? 2 : 1, seg = g->seg;
+        const int seg = g->seg;
+        const bool mine = g->rows > q * kHalf;
         give(turn);
-        [&] {
-        if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(k_full + 8 * (n & 1), (n >> 1) & 1)))) return;
-#pragma unroll 1
-        for (int q = 0; q < halves; ++q) {
-          // the half's queries are in, and the last tile's P (where S goes) has been multiplied
-          const int nq = q ? nq1 : nq0;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_full + 8 * q, (q ? tiles1 : tiles0) & 1) &&
-                                           (nq == 0 || mbar_wait(pv_done + 8 * q, (nq - 1) & 1)));
-          if (!ok) return;
-          ++(q ? tiles1 : tiles0);
-          tc_fence_after();
-          scores(q, n & 1);
-        }
-        umma_commit(k_empty + 8 * (n & 1));
-        // Whichever half is ready goes next: O += P V once its probabilities are there, then, once that has read P
-        // (the next scores go over it), the next chunk's scores.
-        int c0 = 0, c1 = halves == 2 ? 0 : seg;                      // chunk of each half
-        bool w0 = false, w1 = false;                                 // waiting for its product
-        int vs = 0, ks = 0;                                          // halves done with the values, the next keys
-        uint32_t idle = 0;
-        while (c0 < seg || c1 < seg) {
-          bool moved = false;
-#pragma unroll 1
-          for (int q = 0; q < 2; ++q) {
-            const int c = q ? c1 : c0, nq = q ? nq1 : nq0;
-            if (c >= seg) continue;
-            if (!(q ? w1 : w0)) {
-              if (!mbar_test(p_full + 8 * q, nq & 1) || !mbar_test(v_full, (n + c) & 1)) continue;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kChunk / 16; ++k)
-                umma_ts(tmem + 2 * kChunk + q * D, tmem + q * kChunk + 8 * k, dV + (uint32_t)(((k >> 2) * SH::kVPanel + 32 * (k & 3)) >> 4),
-                        SH::kIdescO, c > 0 || k > 0);
-              umma_commit(pv_done + 8 * q);
-              if (++vs == halves) {
-                umma_commit(v_empty);
-                vs = 0;
-              }
-              if (c + 1 < seg) (q ? w1 : w0) = true;
-              else { ++(q ? c1 : c0); ++(q ? nq1 : nq0); }
-            } else {
-              const int buf = (n + c + 1) & 1;
-              if (!mbar_test(pv_done + 8 * q, nq & 1) || !mbar_test(k_full + 8 * buf, ((n + c + 1) >> 1) & 1)) continue;
-              tc_fence_after();
-              scores(q, buf);
-              if (++ks == halves) {
-                umma_commit(k_empty + 8 * buf);
-                ks = 0;
-              }
-              (q ? w1 : w0) = false;
-              ++(q ? c1 : c0);
-              ++(q ? nq1 : nq0);
+        if (!mine) {                                                 // keep the buffers going for the other half
+          for (int c = 0; c < seg && ok; ++c, ++n) {
+            if (lane == 0) {
+              mbar_arrive(k_empty + 8 * (n & 1));
+              mbar_arrive(v_empty);
             }
-            moved = true;
+            __syncwarp();
+            if (wait(k_empty + 8 * (n & 1), n >> 1)) wait(v_empty, n);
           }
-          idle = moved ? 0 : idle + 1;
-          if (idle > kIdlePolls) {
-            ok = false;
-            return;
+          continue;
+        }
+        // the queries are in, and the last tile's P (where S goes) has been multiplied
+        if (!wait(k_full + 8 * (n & 1), n >> 1) || !wait(q_full + 8 * q, tiles++) || (nq && !wait(pv_done + 8 * (2 * q + 1), nq - 1))) break;
+        scores(0, n & 1, false);
+        scores(1, n & 1, true);
+        for (int c = 0; c < seg && ok; ++c, ++n, ++nq) {
+          const int buf = (n + 1) & 1;
+          const bool next = c + 1 < seg;
+          // each step's product once its probabilities are there, then, once that has read P (S goes over it), the
+          // step's scores of the next chunk: they are ready when the other step's softmax is done
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            if (!wait(p_full + 8 * (2 * q + x), nq) || (x == 0 && !wait(v_full, n))) break;
+            product(x, c > 0 || x);
+            if (!next) continue;
+            if ((x == 0 && !wait(k_full + 8 * buf, (n + 1) >> 1)) || !wait(pv_done + 8 * (2 * q + x), nq)) break;
+            scores(x, buf, x);
           }
         }
-        n += seg;
-        }();
       }
       // every MMA issued has completed once done_bar flips
-      umma_commit(done_bar);
-      if (!mbar_wait(done_bar, 0)) ok = false;
+      __syncwarp();
+      if (elect_one()) umma_commit(done_bar + 8 * q);
+      __syncwarp();
+      if (!mbar_wait(done_bar + 8 * q, 0)) ok = false;
     } else if (warp == 14) {
       // ---------------- the walk ----------------
       Segments<kRows, kChunk, kTileCost> sg;
@@ -576,95 +581,105 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
 #pragma unroll 1
       for (int c = 0; c < seg; ++c, ++n, ++nq) {
         const int t0 = (chunk0 + c) * kChunk;
-        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * q, nq & 1));
-        if (!ok) continue;
-        tc_fence_after();
         const float* sc = sscale + (n % kScaleSlots) * 3 * kBlocks;
         uint64_t cf[kBlocks / 2], lv[kBlocks / 2];
-#pragma unroll
-        for (int j = 0; j < kBlocks / 2; ++j) {
-          const float2 ks = *reinterpret_cast<const float2*>(sc + 2 * j), x = *reinterpret_cast<const float2*>(sc + kBlocks + 2 * j);
-          cf[j] = pack2(rowf * ks.x, rowf * ks.y);
-          lv[j] = pack2(x.x, x.y);
-        }
-        uint32_t s[kChunk];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
-        tmem_wait_ld();
-        // the exponents (base 2) of the row's probabilities; pairs of columns, whose blocks repeat every eight columns
-        uint64_t t[kChunk / 2];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < kChunk / 2; ++i)
-          t[i] = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cf[i & 3], lv[i & 3]);
-        if (t0 + kChunk > clear) {
-          const int lim = pos - t0;                                  // the last visible token of the chunk
-#pragma unroll
-          for (int i = 0; i < kChunk / 2; ++i) {
-            float x, y;
-            unpack2(t[i], x, y);
-            const int row = 2 * i, tok = 16 * (row & 7) + (row >> 3);
-            t[i] = pack2(tok > lim ? -INFINITY : x, tok + 16 > lim ? -INFINITY : y);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kChunk / 2; ++i) {
-          float x, y;
-          unpack2(t[i], x, y);
-          asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(x), "f"(y));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-          const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
-          m = nm;
-          l *= f;
-          if (c > 0) {                                               // the products so far are complete (MMA order)
-#pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t o[16];
-              tmem_ld16(tO + 16 * i, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(tO + 16 * i, o);
-            }
-          }
-        }
-        const float neg = m == -INFINITY ? 0.0f : -m;
-        const uint64_t neg2 = pack2(neg, neg);
-        uint64_t acc[kBlocks / 2];
+        uint64_t acc[kBlocks / 2];                                   // sums of p' of the blocks
 #pragma unroll
         for (int j = 0; j < kBlocks / 2; ++j) acc[j] = 0;
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * (2 * q + x), nq & 1));
+          if (!ok) continue;
+          tc_fence_after();
+          uint32_t s[kSub];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t pk[16];
+          for (int i = 0; i < 2; ++i) tmem_ld32(tS + x * kSub + 32 * i, s + 32 * i);
+          if (x == 0) {                                              // (while the scores are on their way)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x, y;
-            unpack2(add2(t[16 * h + i], neg2), x, y);
-            x = exp2_approx(x);
-            y = exp2_approx(y);
-            acc[i & 3] = add2(acc[i & 3], pack2(x, y));
-            pk[i] = pack_f16(x, y);
+            for (int j = 0; j < kBlocks / 2; ++j) {
+              const float2 ks = *reinterpret_cast<const float2*>(sc + 2 * j), y = *reinterpret_cast<const float2*>(sc + kBlocks + 2 * j);
+              cf[j] = pack2(rowf * ks.x, rowf * ks.y);
+              lv[j] = pack2(y.x, y.y);
+            }
           }
-          tmem_st16(tS + 16 * h, pk);
+          tmem_wait_ld();
+          // the exponents (base 2) of the row's probabilities; pairs of columns, whose blocks repeat every eight columns
+          uint64_t t[kSub / 2];
+#pragma unroll
+          for (int i = 0; i < kSub / 2; ++i)
+            t[i] = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cf[i & 3], lv[i & 3]);
+          if (t0 + kChunk > clear) {
+            const int lim = pos - t0 - 8 * x;                        // the last visible token, less the step's first
+#pragma unroll
+            for (int i = 0; i < kSub / 2; ++i) {
+              float e, f;
+              unpack2(t[i], e, f);
+              const int row = 2 * i, tok = 16 * (row & 7) + (row >> 3);
+              t[i] = pack2(tok > lim ? -INFINITY : e, tok + 16 > lim ? -INFINITY : f);
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kSub / 2; ++i) {
+            float e, f;
+            unpack2(t[i], e, f);
+            asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(e), "f"(f));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+            const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
+            const uint64_t f2 = pack2(f, f);
+            m = nm;
+            l *= f;
+#pragma unroll
+            for (int j = 0; j < kBlocks / 2; ++j) acc[j] = mul2(acc[j], f2);
+            if (c > 0 || x > 0) {                                    // after the products so far
+              ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done + 8 * (2 * q + (x ^ 1)), (x ? nq : nq - 1) & 1));
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(tO + 16 * i, o);
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.0f : -m;
+          const uint64_t neg2 = pack2(neg, neg);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float e, f;
+              unpack2(add2(t[16 * h + i], neg2), e, f);
+              e = exp2_approx(e);
+              f = exp2_approx(f);
+              acc[i & 3] = add2(acc[i & 3], pack2(e, f));
+              pk[i] = pack_f16(e, f);
+            }
+            tmem_st16(tS + x * kSub + 16 * h, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 8 * (2 * q + x));
         }
 #pragma unroll
         for (int j = 0; j < kBlocks / 2; ++j) {
-          float x, y;
-          unpack2(acc[j], x, y);
+          float e, f;
+          unpack2(acc[j], e, f);
           const float2 iv = *reinterpret_cast<const float2*>(sc + 2 * kBlocks + 2 * j);
-          l = fmaf(x, iv.x, fmaf(y, iv.y, l));
+          l = fmaf(e, iv.x, fmaf(f, iv.y, l));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * q);
       }
       // ---- the tile's end ----
       const int c0 = g->c0, c1 = g->c1;
       const bool whole = c0 == c1;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done + 8 * q, (nq - 1) & 1));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done + 8 * (2 * q + 1), (nq - 1) & 1));
       tc_fence_after();
       // element d of row r of a partial result at [d / 4][r][d % 4]: neighbouring rows are neighbours
       float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes) + (int64_t)q * SH::kPartFloats;
