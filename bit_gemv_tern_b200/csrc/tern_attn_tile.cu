@@ -49,10 +49,11 @@ constexpr int kTileCost = 2;
 constexpr int kThreads = 512;
 constexpr int kDecWarps = 4;
 constexpr int kPanel = 128 * 128;                 // a swizzled panel of 128 rows x 64 fp16
-// block scales of this many chunks: values lag keys by one chunk and the ring of codes is two, so three are in use
-constexpr int kScaleSlots = 4;
+// block scales of this many chunks: codes in flight, two expanded, one in the softmax and the one before it, whose sums
+// a thread may still be scaling; a power of two
+constexpr int kScaleSlots = 8;
 // registers a thread of the softmax warpgroups and of the others: they add up to what the launch has
-constexpr int kRegsSoftmax = 144, kRegsOther = 112;
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 static_assert((kRegsSoftmax + kRegsOther) * (kThreads / 2) == 128 * kThreads, "register split");
 
 // A piece of a tile: what the warps need to know of it.
@@ -75,10 +76,10 @@ struct Tile {
   static constexpr int kVPanel = D * 128;                           // D rows x 64 tokens
   static constexpr int kV = 2 * kVPanel;
   static constexpr int kRaw = kChunk * D;                           // codes of a chunk's keys
-  static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffRaw = kOffV + kV;
-  static constexpr int kOffScale = kOffRaw + 2 * 2 * kRaw;          // [slot][ks, log2 vs, 1 / vs][block]
+  static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffRaw = kOffV + 2 * kV;
+  static constexpr int kOffScale = kOffRaw + 2 * kRaw;           // [slot][ks, log2 vs, 1 / vs][block]
   static constexpr int kOffBar = kOffScale + kScaleSlots * 3 * kBlocks * 4;
-  static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 4 + 4 + 4 + 2 + 2 * kSegments;
+  static constexpr int kBars = 1 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 2 + 4 + 4 + 4 + 2 + 2 * kSegments;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kPartFloats = kHalf * D + 2 * kHalf;         // a half's partial result
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kSub >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
@@ -242,9 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
   uint8_t* sm = smem_raw + (base - raw0);
   float* sscale = reinterpret_cast<float*>(sm + SH::kOffScale);
   const uint32_t sQ = base, sK = base + SH::kOffK, sV = base + SH::kOffV, sRaw = base + SH::kOffRaw;
-  const uint32_t kr_full = base + SH::kOffBar, kr_empty = kr_full + 16, vr_full = kr_empty + 16, vr_empty = vr_full + 16;
-  const uint32_t k_full = vr_empty + 16, k_empty = k_full + 16;
-  const uint32_t v_full = k_empty + 16, v_empty = v_full + 8, q_full = v_empty + 8;
+  const uint32_t kr_full = base + SH::kOffBar, kr_empty = kr_full + 8, vr_full = kr_empty + 8, vr_empty = vr_full + 8;
+  const uint32_t k_full = vr_empty + 8, k_empty = k_full + 16;
+  const uint32_t v_full = k_empty + 16, v_empty = v_full + 16, q_full = v_empty + 16;
   const uint32_t s_full = q_full + 16, p_full = s_full + 32;       // [half][step]
   const uint32_t pv_done = p_full + 32, done_bar = pv_done + 32;
   const uint32_t seg_full = done_bar + 16, seg_empty = seg_full + 8 * kSegments, tmem_slot = seg_empty + 8 * kSegments;
@@ -256,12 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
 
   if (threadIdx.x == 12 * 32) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kr_full + 8 * i, 1);
-      mbar_init(kr_empty + 8 * i, kDecWarps);
-      mbar_init(vr_full + 8 * i, 1);
-      mbar_init(vr_empty + 8 * i, kDecWarps);
       mbar_init(k_full + 8 * i, kDecWarps);
       mbar_init(k_empty + 8 * i, 2);
+      mbar_init(v_full + 8 * i, kDecWarps);
+      mbar_init(v_empty + 8 * i, 2);
       mbar_init(q_full + 8 * i, 4);
     }
     for (int i = 0; i < 4; ++i) {
@@ -269,8 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       mbar_init(p_full + 8 * i, 4);
       mbar_init(pv_done + 8 * i, 1);
     }
-    mbar_init(v_full, kDecWarps);
-    mbar_init(v_empty, 2);
+    mbar_init(kr_full, 1);
+    mbar_init(kr_empty, kDecWarps);
+    mbar_init(vr_full, 1);
+    mbar_init(vr_empty, kDecWarps);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(seg_full + 8 * i, 1);
       mbar_init(seg_empty + 8 * i, kSegWarps);
@@ -309,19 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp < 12) {
-      // ---------------- codes to operand tiles: the next chunk's keys before this one's values ----------------
+      // ---------------- codes to operand tiles ----------------
       const int wd = warp - 8;
-      auto values = [&](int i) {                                     // of chunk i
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(vr_full + 8 * (i & 1), (i >> 1) & 1) && (i < 1 || mbar_wait(v_empty, (i - 1) & 1)));
-        if (!ok) return;
-        expand_values<D>(sRaw + (2 + (i & 1)) * SH::kRaw, sV, wd, lane);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(v_full);
-          mbar_arrive(vr_empty + 8 * (i & 1));
-        }
-      };
       int i = 0;                                                     // chunk
       for (int turn = 0; ok; ++turn) {
         const Segment* g = take(turn, ok);
@@ -330,20 +320,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
         give(turn);
         for (; i < end && ok; ++i) {
           const int s = i & 1;
-          ok = mbar_wait(kr_full + 8 * s, (i >> 1) & 1) && (i < 2 || mbar_wait(k_empty + 8 * s, ((i >> 1) - 1) & 1));
+          ok = mbar_wait(kr_full, i & 1) && (i < 2 || mbar_wait(k_empty + 8 * s, ((i >> 1) - 1) & 1));
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-          expand_keys<D>(sRaw + s * SH::kRaw, sK + s * SH::kK, wd, lane);
+          expand_keys<D>(sRaw, sK + s * SH::kK, wd, lane);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(k_full + 8 * s);
-            mbar_arrive(kr_empty + 8 * s);
+            mbar_arrive(kr_empty);
           }
-          if (i > 0) values(i - 1);
+          ok = mbar_wait(vr_full, i & 1) && (i < 2 || mbar_wait(v_empty + 8 * s, ((i >> 1) - 1) & 1));
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          expand_values<D>(sRaw + SH::kRaw, sV + s * SH::kV, wd, lane);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(v_full + 8 * s);
+            mbar_arrive(vr_empty);
+          }
         }
       }
-      if (ok && i > 0) values(i - 1);
     } else if (warp == 12) {
       // ---------------- producer ----------------
       int n = 0, nk = 0;                                             // chunks issued: values, keys
@@ -374,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
               }
             }
           }
-          const int s = n & 1, slot = n % kScaleSlots;
-          if (n >= 2 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(kr_empty + 8 * s, ((n >> 1) - 1) & 1)))) break;
+          const int slot = n % kScaleSlots;
+          if (n >= 1 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(kr_empty, (n - 1) & 1)))) break;
           // blocks 0..7 of the chunk to lanes 0..7
           const int src = 8 * at + (lane & 7);
           const int r = __shfl_sync(0xFFFFFFFFu, row, src);
@@ -392,23 +390,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
             sc[2 * kBlocks] = r >= 0 ? __fdividef(1.0f, v) : 0.0f;
           }
           __syncwarp();
-          const uint32_t bytes = __popc(have) * p.box * D, dst = sRaw + s * SH::kRaw + lane * TERN_KV_BLOCK * D;
-          if (lane == 0) mbar_arrive_expect_tx(kr_full + 8 * s, bytes);
+          const uint32_t bytes = __popc(have) * p.box * D, dst = sRaw + lane * TERN_KV_BLOCK * D;
+          if (lane == 0) mbar_arrive_expect_tx(kr_full, bytes);
           __syncwarp();
-          if (copies) tma_load_2d(dst, &a.kmap, 0, r, kr_full + 8 * s);
-          if (n >= 2 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(vr_empty + 8 * s, ((n >> 1) - 1) & 1)))) {
-            ++nk;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(vr_full + 8 * s, bytes);
-          __syncwarp();
-          if (copies) tma_load_2d(dst + 2 * SH::kRaw, &a.vmap, 0, r, vr_full + 8 * s);
+          if (copies) tma_load_2d(dst, &a.kmap, 0, r, kr_full);
           ++nk;
+          if (n >= 1 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(vr_empty, (n - 1) & 1)))) break;
+          if (lane == 0) mbar_arrive_expect_tx(vr_full, bytes);
+          __syncwarp();
+          if (copies) tma_load_2d(dst + SH::kRaw, &a.vmap, 0, r, vr_full);
         }
       }
       // do not leave with copies in flight (bounded, also after a give-up)
-      for (int r = nk > 2 ? nk - 2 : 0; r < nk; ++r)
-        if (!mbar_wait(kr_full + 8 * (r & 1), (r >> 1) & 1) || (r < n && !mbar_wait(vr_full + 8 * (r & 1), (r >> 1) & 1))) { ok = false; break; }
+      if ((nk && !mbar_wait(kr_full, (nk - 1) & 1)) || (n && !mbar_wait(vr_full, (n - 1) & 1))) ok = false;
     } else if (warp == 13 || warp == 15) {
       // ---------------- MMA issue, a warp for each half ----------------
       const uint64_t dQ = umma_desc(sQ), dK = umma_desc(sK), dV = umma_desc(sV);     // + offset / 16: the address field
@@ -429,15 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
         __syncwarp();
       };
       // O += P V of step x; more: O holds earlier products
-      auto product = [&](int x, bool more) {
+      auto product = [&](int x, int buf, bool more) {
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t b = dV + (uint32_t)(x * (SH::kVPanel >> 4));
+          const uint64_t b = dV + (uint32_t)(buf * (SH::kV >> 4) + x * (SH::kVPanel >> 4));
 #pragma unroll
           for (int k = 0; k < kSub / 16; ++k)
             umma_ts(tO, tS + x * kSub + 8 * k, b + (uint32_t)(32 * k >> 4), SH::kIdescO, k > 0 ? 1u : (uint32_t)more);
           umma_commit(pv_done + 8 * (2 * q + x));
-          if (x) umma_commit(v_empty);
+          if (x) umma_commit(v_empty + 8 * buf);
         }
         __syncwarp();
       };
@@ -456,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           for (int c = 0; c < seg && ok; ++c, ++n) {
             if (lane == 0) {
               mbar_arrive(k_empty + 8 * (n & 1));
-              mbar_arrive(v_empty);
+              mbar_arrive(v_empty + 8 * (n & 1));
             }
             __syncwarp();
-            if (wait(k_empty + 8 * (n & 1), n >> 1)) wait(v_empty, n);
+            if (wait(k_empty + 8 * (n & 1), n >> 1)) wait(v_empty + 8 * (n & 1), n >> 1);
           }
           continue;
         }
@@ -474,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           // step's scores of the next chunk: they are ready when the other step's softmax is done
 #pragma unroll 1
           for (int x = 0; x < 2; ++x) {
-            if (!wait(p_full + 8 * (2 * q + x), nq) || (x == 0 && !wait(v_full, n))) break;
-            product(x, c > 0 || x);
+            if (!wait(p_full + 8 * (2 * q + x), nq) || (x == 0 && !wait(v_full + 8 * (n & 1), n >> 1))) break;
+            product(x, n & 1, c > 0 || x);
             if (!next) continue;
             if ((x == 0 && !wait(k_full + 8 * buf, (n + 1) >> 1)) || !wait(pv_done + 8 * (2 * q + x), nq)) break;
             scores(x, buf, x);
@@ -553,24 +547,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       float rowf;
       {
         uint4 v[D / 8];
-        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          v[i] = r < valid ? ld_nc(p.q + at * D + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i = 0; i < D / 8; ++i) v[i] = r < valid ? ld_nc(p.q + at * D + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        __nv_bfloat162 top2 = __float2bfloat162_rn(0.0f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-        }
-        const int E = absmax_exponent(top);
-        const float up = exp2f_i(14 - E);
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top2 = __hmax2_nan(top2, __habs2(reinterpret_cast<const __nv_bfloat162*>(&v[i])[e]));
+        const int E = absmax_exponent(fmaxf(__low2float(top2), __high2float(top2)));
+        const __nv_bfloat162 up = __float2bfloat162_rn(exp2f_i(14 - E));             // a power of two: exact products
         rowf = p.scale * kLog2e * exp2f_i(E - 14);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = pack_f16(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __bfloat1622float2(__hmul2(reinterpret_cast<const __nv_bfloat162*>(&v[i])[e], up));
+            h[e] = pack_f16(f.x, f.y);
+          }
           sts128(sQ + q * SH::kQ + (i >> 3) * kPanel + r * 128 + (((i & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -727,31 +721,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           __threadfence();
           if (lane == 0) *counter = 0;
           float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
           for (int i = c0; i <= c1; ++i) top = fmaxf(top, __ldcg(part_of(i) + kHalf * D + r));
+#pragma unroll 4
           for (int i = c0; i <= c1; ++i) {
             const float mi = __ldcg(part_of(i) + kHalf * D + r);
             sum = fmaf(__ldcg(part_of(i) + kHalf * D + kHalf + r), mi == -INFINITY ? 0.0f : exp2_approx(mi - top), sum);
           }
           const float iv = inv_of(sum);
+          constexpr int kTake = 16;                                  // float4s of a partial result in flight
 #pragma unroll 1
-          for (int e = 0; e < D / 4; e += 4) {
-            float4 v[4];
+          for (int e = 0; e < D / 4; e += kTake) {
+            float4 v[kTake];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k = 0; k < kTake; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
             for (int i = c0; i <= c1; ++i) {
               const float* y = part_of(i);
               const float mi = __ldcg(y + kHalf * D + r), f = mi == -INFINITY ? 0.0f : exp2_approx(mi - top) * iv;
+              float4 u[kTake];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(y + ((e + k) * kHalf + r) * 4));
-                v[k].x = fmaf(u.x, f, v[k].x); v[k].y = fmaf(u.y, f, v[k].y); v[k].z = fmaf(u.z, f, v[k].z); v[k].w = fmaf(u.w, f, v[k].w);
+              for (int k = 0; k < kTake; ++k) u[k] = __ldcg(reinterpret_cast<const float4*>(y + ((e + k) * kHalf + r) * 4));
+#pragma unroll
+              for (int k = 0; k < kTake; ++k) {
+                v[k].x = fmaf(u[k].x, f, v[k].x); v[k].y = fmaf(u[k].y, f, v[k].y);
+                v[k].z = fmaf(u[k].z, f, v[k].z); v[k].w = fmaf(u[k].w, f, v[k].w);
               }
             }
             if (r < valid) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(v[k].x, v[k].y), z = __floats2bfloat162_rn(v[k].z, v[k].w);
-                *reinterpret_cast<uint2*>(p.out + at * D + 4 * (e + k)) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&z));
+              for (int k = 0; k < kTake; k += 2) {
+                const __nv_bfloat162 x0 = __floats2bfloat162_rn(v[k].x, v[k].y), x1 = __floats2bfloat162_rn(v[k].z, v[k].w);
+                const __nv_bfloat162 x2 = __floats2bfloat162_rn(v[k + 1].x, v[k + 1].y), x3 = __floats2bfloat162_rn(v[k + 1].z, v[k + 1].w);
+                *reinterpret_cast<uint4*>(p.out + at * D + 4 * (e + k)) =
+                    make_uint4(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1),
+                               *reinterpret_cast<const uint32_t*>(&x2), *reinterpret_cast<const uint32_t*>(&x3));
               }
             }
           }
