@@ -14,9 +14,8 @@
 //   warp 12     TMA of the raw codes (boxes of up to 64 tokens of a page), block scales;
 //   warp 14     walks the CTA's range and hands the other warps their segments through a ring;
 //   warps 13, 15  issue the tcgen05.mma kind::f16 of a half each: S = Q K^T (A = Q and B = K from shared
-//               memory), O += P V (A = P from TMEM, B = V^T), in steps of 64 of a chunk's tokens: while
-//               the softmax works on one step's scores, the other step is multiplied and its next
-//               scores are made.
+//               memory), O += P V (A = P from TMEM, B = V^T). While one half's softmax runs, the other
+//               half's products do.
 // TMEM: S of the two halves (128 columns each, P over them), O of the two halves (128 each): all 512.
 // Token order: the key tile's row 8 o + j holds token 16 j + o of the chunk, so that the transposition of the
 // values reads and writes shared memory without bank conflicts; column r of S is then of block r % 8, and the
@@ -43,7 +42,6 @@ namespace {
 constexpr int kRows = 256, kHalf = 128;           // rows of a tile, of an MMA
 constexpr int kChunk = 128;                       // tokens of a chunk
 constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
-constexpr int kSub = 64;                          // columns of S that a softmax step and a pair of products take
 // What a tile costs beside its chunks (queries in, results out), in chunks of about a microsecond.
 constexpr int kTileCost = 2;
 constexpr int kThreads = 512;
@@ -53,7 +51,7 @@ constexpr int kPanel = 128 * 128;                 // a swizzled panel of 128 row
 // a thread may still be scaling; a power of two
 constexpr int kScaleSlots = 8;
 // registers a thread of the softmax warpgroups and of the others: they add up to what the launch has
-constexpr int kRegsSoftmax = 168, kRegsOther = 88;
+constexpr int kRegsSoftmax = 184, kRegsOther = 72;
 static_assert((kRegsSoftmax + kRegsOther) * (kThreads / 2) == 128 * kThreads, "register split");
 
 // A piece of a tile: what the warps need to know of it.
@@ -79,10 +77,10 @@ struct Tile {
   static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kK, kOffRaw = kOffV + 2 * kV;
   static constexpr int kOffScale = kOffRaw + 2 * kRaw;           // [slot][ks, log2 vs, 1 / vs][block]
   static constexpr int kOffBar = kOffScale + kScaleSlots * 3 * kBlocks * 4;
-  static constexpr int kBars = 1 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 2 + 4 + 4 + 4 + 2 + 2 * kSegments;
+  static constexpr int kBars = 1 + 1 + 1 + 1 + 2 + 2 + 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 * kSegments;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kPartFloats = kHalf * D + 2 * kHalf;         // a half's partial result
-  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kSub >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
+  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kChunk >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
 };
 
@@ -174,11 +172,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -246,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
   const uint32_t kr_full = base + SH::kOffBar, kr_empty = kr_full + 8, vr_full = kr_empty + 8, vr_empty = vr_full + 8;
   const uint32_t k_full = vr_empty + 8, k_empty = k_full + 16;
   const uint32_t v_full = k_empty + 16, v_empty = v_full + 16, q_full = v_empty + 16;
-  const uint32_t s_full = q_full + 16, p_full = s_full + 32;       // [half][step]
-  const uint32_t pv_done = p_full + 32, done_bar = pv_done + 32;
+  const uint32_t s_full = q_full + 16, p_full = s_full + 16;         // p_full: [half][half of the chunk]
+  const uint32_t pv_done = p_full + 32, done_bar = pv_done + 16;
   const uint32_t seg_full = done_bar + 16, seg_empty = seg_full + 8 * kSegments, tmem_slot = seg_empty + 8 * kSegments;
   __shared__ Plan plan;
   __shared__ longlong2 warp_sums[kThreads / 32];
@@ -263,11 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       mbar_init(v_empty + 8 * i, 2);
       mbar_init(q_full + 8 * i, 4);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 4);
       mbar_init(pv_done + 8 * i, 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 4);
     mbar_init(kr_full, 1);
     mbar_init(kr_empty, kDecWarps);
     mbar_init(vr_full, 1);
@@ -408,30 +401,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       const uint64_t dQ = umma_desc(sQ), dK = umma_desc(sK), dV = umma_desc(sV);     // + offset / 16: the address field
       const int q = warp == 15;
       const uint32_t tS = tmem + q * kChunk, tO = tmem + 2 * kChunk + q * D;
-      // the scores of step x (64 of the chunk's tokens) from key buffer `buf`; last: the buffer is done with
-      auto scores = [&](int x, int buf, bool last) {
+      // the scores of a chunk from key buffer `buf`
+      auto scores = [&](int buf) {
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t a = dQ + (uint32_t)(q * (SH::kQ >> 4)), b = dK + (uint32_t)(buf * (SH::kK >> 4) + x * (kSub * 128 >> 4));
+          const uint64_t a = dQ + (uint32_t)(q * (SH::kQ >> 4)), b = dK + (uint32_t)(buf * (SH::kK >> 4));
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_ss(tS + x * kSub, a + (uint32_t)(((k >> 2) * kPanel + 32 * (k & 3)) >> 4),
-                    b + (uint32_t)(((k >> 2) * kPanel + 32 * (k & 3)) >> 4), SH::kIdescS, k > 0);
-          umma_commit(s_full + 8 * (2 * q + x));
-          if (last) umma_commit(k_empty + 8 * buf);
+            umma_ss(tS, a + (uint32_t)(((k >> 2) * kPanel + 32 * (k & 3)) >> 4), b + (uint32_t)(((k >> 2) * kPanel + 32 * (k & 3)) >> 4),
+                    SH::kIdescS, k > 0);
+          umma_commit(s_full + 8 * q);
+          umma_commit(k_empty + 8 * buf);
         }
         __syncwarp();
       };
-      // O += P V of step x; more: O holds earlier products
+      // O += P V of half x of the chunk; more: O holds earlier products
       auto product = [&](int x, int buf, bool more) {
         tc_fence_after();
         if (elect_one()) {
           const uint64_t b = dV + (uint32_t)(buf * (SH::kV >> 4) + x * (SH::kVPanel >> 4));
 #pragma unroll
-          for (int k = 0; k < kSub / 16; ++k)
-            umma_ts(tO, tS + x * kSub + 8 * k, b + (uint32_t)(32 * k >> 4), SH::kIdescO, k > 0 ? 1u : (uint32_t)more);
-          umma_commit(pv_done + 8 * (2 * q + x));
-          if (x) umma_commit(v_empty + 8 * buf);
+          for (int k = 0; k < 4; ++k)
+            umma_ts(tO, tS + 32 * x + 8 * k, b + (uint32_t)(32 * k >> 4), SH::kIdescO, k > 0 ? 1u : (uint32_t)more);
+          if (x) {
+            umma_commit(pv_done + 8 * q);
+            umma_commit(v_empty + 8 * buf);
+          }
         }
         __syncwarp();
       };
@@ -458,21 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           continue;
         }
         // the queries are in, and the last tile's P (where S goes) has been multiplied
-        if (!wait(k_full + 8 * (n & 1), n >> 1) || !wait(q_full + 8 * q, tiles++) || (nq && !wait(pv_done + 8 * (2 * q + 1), nq - 1))) break;
-        scores(0, n & 1, false);
-        scores(1, n & 1, true);
-        for (int c = 0; c < seg && ok; ++c, ++n, ++nq) {
-          const int buf = (n + 1) & 1;
-          const bool next = c + 1 < seg;
-          // each step's product once its probabilities are there, then, once that has read P (S goes over it), the
-          // step's scores of the next chunk: they are ready when the other step's softmax is done
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            if (!wait(p_full + 8 * (2 * q + x), nq) || (x == 0 && !wait(v_full + 8 * (n & 1), n >> 1))) break;
-            product(x, n & 1, c > 0 || x);
-            if (!next) continue;
-            if ((x == 0 && !wait(k_full + 8 * buf, (n + 1) >> 1)) || !wait(pv_done + 8 * (2 * q + x), nq)) break;
-            scores(x, buf, x);
+        if (!wait(k_full + 8 * (n & 1), n >> 1) || !wait(q_full + 8 * q, tiles++) || (nq && !wait(pv_done + 8 * q, nq - 1))) break;
+        scores(n & 1);
+        for (int c = 0; c < seg; ++c, ++n, ++nq) {
+          if (!wait(v_full + 8 * (n & 1), n >> 1) || !wait(p_full + 16 * q, nq)) break;
+          product(0, n & 1, c > 0);
+          if (!wait(p_full + 16 * q + 8, nq)) break;
+          product(1, n & 1, true);
+          if (c + 1 < seg) {
+            // the next scores go over P once that has been read
+            if (!wait(k_full + 8 * ((n + 1) & 1), (n + 1) >> 1) || !wait(pv_done + 8 * q, nq)) break;
+            scores((n + 1) & 1);
           }
         }
       }
@@ -575,105 +566,97 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
 #pragma unroll 1
       for (int c = 0; c < seg; ++c, ++n, ++nq) {
         const int t0 = (chunk0 + c) * kChunk;
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * q, nq & 1));
+        if (!ok) continue;
+        tc_fence_after();
+        uint32_t s[kChunk];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
         const float* sc = sscale + (n % kScaleSlots) * 3 * kBlocks;
         uint64_t cf[kBlocks / 2], lv[kBlocks / 2];
+#pragma unroll
+        for (int j = 0; j < kBlocks / 2; ++j) {
+          const float2 ks = *reinterpret_cast<const float2*>(sc + 2 * j), x = *reinterpret_cast<const float2*>(sc + kBlocks + 2 * j);
+          cf[j] = pack2(rowf * ks.x, rowf * ks.y);
+          lv[j] = pack2(x.x, x.y);
+        }
+        tmem_wait_ld();
+        // the exponents (base 2) of the row's probabilities; pairs of columns, whose blocks repeat every eight columns
+        uint64_t t[kChunk / 2];
+#pragma unroll
+        for (int i = 0; i < kChunk / 2; ++i)
+          t[i] = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cf[i & 3], lv[i & 3]);
+        if (t0 + kChunk > clear) {
+          const int lim = pos - t0;                                  // the last visible token of the chunk
+#pragma unroll
+          for (int i = 0; i < kChunk / 2; ++i) {
+            float x, y;
+            unpack2(t[i], x, y);
+            const int row = 2 * i, tok = 16 * (row & 7) + (row >> 3);
+            t[i] = pack2(tok > lim ? -INFINITY : x, tok + 16 > lim ? -INFINITY : y);
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kChunk / 2; ++i) {
+          float x, y;
+          unpack2(t[i], x, y);
+          asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(x), "f"(y));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+          const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
+          m = nm;
+          l *= f;
+          if (c > 0) {                                               // the products so far are complete: the scores waited for them
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tO + 16 * i, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.0f : -m;
+        const uint64_t neg2 = pack2(neg, neg);
         uint64_t acc[kBlocks / 2];                                   // sums of p' of the blocks
 #pragma unroll
         for (int j = 0; j < kBlocks / 2; ++j) acc[j] = 0;
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * (2 * q + x), nq & 1));
-          if (!ok) continue;
-          tc_fence_after();
-          uint32_t s[kSub];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_ld32(tS + x * kSub + 32 * i, s + 32 * i);
-          if (x == 0) {                                              // (while the scores are on their way)
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
 #pragma unroll
-            for (int j = 0; j < kBlocks / 2; ++j) {
-              const float2 ks = *reinterpret_cast<const float2*>(sc + 2 * j), y = *reinterpret_cast<const float2*>(sc + kBlocks + 2 * j);
-              cf[j] = pack2(rowf * ks.x, rowf * ks.y);
-              lv[j] = pack2(y.x, y.y);
-            }
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack2(add2(t[16 * h + i], neg2), x, y);
+            x = exp2_approx(x);
+            y = exp2_approx(y);
+            acc[i & 3] = add2(acc[i & 3], pack2(x, y));
+            pk[i] = pack_f16(x, y);
           }
-          tmem_wait_ld();
-          // the exponents (base 2) of the row's probabilities; pairs of columns, whose blocks repeat every eight columns
-          uint64_t t[kSub / 2];
-#pragma unroll
-          for (int i = 0; i < kSub / 2; ++i)
-            t[i] = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cf[i & 3], lv[i & 3]);
-          if (t0 + kChunk > clear) {
-            const int lim = pos - t0 - 8 * x;                        // the last visible token, less the step's first
-#pragma unroll
-            for (int i = 0; i < kSub / 2; ++i) {
-              float e, f;
-              unpack2(t[i], e, f);
-              const int row = 2 * i, tok = 16 * (row & 7) + (row >> 3);
-              t[i] = pack2(tok > lim ? -INFINITY : e, tok + 16 > lim ? -INFINITY : f);
-            }
+          tmem_st16(tS + 16 * h, pk);
+          if (h & 1) {                                               // a half of the chunk's probabilities is there
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 16 * q + 8 * (h >> 1));
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < kSub / 2; ++i) {
-            float e, f;
-            unpack2(t[i], e, f);
-            asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(e), "f"(f));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-            const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
-            const uint64_t f2 = pack2(f, f);
-            m = nm;
-            l *= f;
-#pragma unroll
-            for (int j = 0; j < kBlocks / 2; ++j) acc[j] = mul2(acc[j], f2);
-            if (c > 0 || x > 0) {                                    // after the products so far
-              ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done + 8 * (2 * q + (x ^ 1)), (x ? nq : nq - 1) & 1));
-              tc_fence_after();
-#pragma unroll 1
-              for (int i = 0; i < D / 16; ++i) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * i, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(tO + 16 * i, o);
-              }
-            }
-          }
-          const float neg = m == -INFINITY ? 0.0f : -m;
-          const uint64_t neg2 = pack2(neg, neg);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float e, f;
-              unpack2(add2(t[16 * h + i], neg2), e, f);
-              e = exp2_approx(e);
-              f = exp2_approx(f);
-              acc[i & 3] = add2(acc[i & 3], pack2(e, f));
-              pk[i] = pack_f16(e, f);
-            }
-            tmem_st16(tS + x * kSub + 16 * h, pk);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + 8 * (2 * q + x));
         }
 #pragma unroll
         for (int j = 0; j < kBlocks / 2; ++j) {
-          float e, f;
-          unpack2(acc[j], e, f);
+          float x, y;
+          unpack2(acc[j], x, y);
           const float2 iv = *reinterpret_cast<const float2*>(sc + 2 * kBlocks + 2 * j);
-          l = fmaf(e, iv.x, fmaf(f, iv.y, l));
+          l = fmaf(x, iv.x, fmaf(y, iv.y, l));
         }
       }
       // ---- the tile's end ----
       const int c0 = g->c0, c1 = g->c1;
       const bool whole = c0 == c1;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done + 8 * (2 * q + 1), (nq - 1) & 1));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done + 8 * q, (nq - 1) & 1));
       tc_fence_after();
       // element d of row r of a partial result at [d / 4][r][d % 4]: neighbouring rows are neighbours
       float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes) + (int64_t)q * SH::kPartFloats;
