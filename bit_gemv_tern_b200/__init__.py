@@ -549,22 +549,24 @@ class QkvSpec:
         for g, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
             if g is not None:
                 _want(g, what, (torch.bfloat16,), (self.head_dim,), self.device)
-        self._c = _Qkv(None, TERN_ELEM_F32, self.q_heads, self.kv_heads, self.head_dim, 0, _ptr(q_gain), _ptr(k_gain),
-                       float(eps), _ptr(freq))
+        self._tail = (self.q_heads, self.kv_heads, self.head_dim)
+        self._ptrs = (_ptr(q_gain), _ptr(k_gain), float(eps), _ptr(freq))
+        self.eps, self.index, self.i32 = float(eps), freq.get_device(), torch.int32
         self._types = {torch.float32: TERN_ELEM_F32, torch.bfloat16: TERN_ELEM_BF16}
 
     def _at(self, src, heads_per_kv: int):
-        """The descriptor of rows src [rows, width] (any row stride the library takes)."""
+        """The descriptor of rows src [rows, width] (any row stride the library takes), and how many they are."""
         kind = self._types.get(src.dtype)
-        if kind is None:
-            raise ValueError(f"src: dtype {src.dtype}, expected torch.float32 or torch.bfloat16")
-        if src.dim() != 2 or src.shape[1] < (self.q_heads + heads_per_kv * self.kv_heads) * self.head_dim or \
-                src.stride(1) != 1 or src.device != self.device:
-            raise ValueError("src: expected rows [rows, >= heads * head_dim] with unit column stride on the spec's device")
-        c = _Qkv.from_buffer_copy(self._c)
-        c.src_dev, c.src_type = src.data_ptr(), kind
-        c.row_stride = src.stride(0) if src.shape[0] > 1 else max(src.stride(0), src.shape[1] + -src.shape[1] % 4)
-        return c
+        if kind is None or src.dim() != 2 or src.get_device() != self.index:
+            raise ValueError(f"src: expected float32 or bfloat16 rows [rows, heads * head_dim] on cuda:{self.index}")
+        rows, width = src.shape
+        stride, unit = src.stride()
+        if width < (self.q_heads + heads_per_kv * self.kv_heads) * self.head_dim or unit != 1:
+            raise ValueError("src: expected at least heads * head_dim columns of unit stride")
+        if rows <= 1:                                  # a single row's stride is never used
+            stride = max(stride, width + -width % 4)
+            stride += -stride % 4
+        return _Qkv(src.data_ptr(), kind, *self._tail, stride, *self._ptrs), rows
 
 
 class KvCache:
@@ -577,7 +579,7 @@ class KvCache:
             raise ValueError("k: expected int8 [pages, kv_heads, page_size, head_dim] with page_size a multiple of 16")
         self.pages, self.kv_heads, self.page_size, self.head_dim = (int(n) for n in k.shape)
         _want(k, "k", (torch.int8,))
-        self.device = k.device
+        self.device, self.index, self.f32 = k.device, k.get_device(), torch.float32
         _want(v, "v", (torch.int8,), k.shape, self.device)
         for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _want(s, what, (torch.float32,), (self.pages, self.kv_heads, self.page_size // TERN_KV_BLOCK), self.device)
@@ -605,7 +607,7 @@ class KvBatch:
         import torch
         i32 = (torch.int32,)
         _want(kv_len, "kv_len", i32, (None,))
-        self.batch, self.rows, self.device = int(kv_len.shape[0]), int(rows), kv_len.device
+        self.batch, self.rows, self.device, self.index = int(kv_len.shape[0]), int(rows), kv_len.device, kv_len.get_device()
         _want(row_start, "row_start", i32, (self.batch + 1,), self.device)
         _want(page_table, "page_table", i32, (self.batch, None), self.device)
         self.row_start, self.kv_len, self.page_table = row_start, kv_len, page_table
@@ -613,25 +615,44 @@ class KvBatch:
         self._ref = ctypes.byref(self._c)
 
 
-def _heads_out(t, what, rows, heads, head_dim, device):
-    import torch
-    if t.dtype is not torch.bfloat16 or t.device != device or not t.is_contiguous() or t.numel() != rows * heads * head_dim:
-        raise ValueError(f"{what}: expected contiguous bfloat16 [{rows}, {heads}, {head_dim}] on {device}")
+# The calls below stand between kernels of a few microseconds, so their checks are kept to cheap ones.
+
+def _heads_out(t, what, rows, heads, head_dim, index):
+    """Address of a contiguous bf16 tensor of rows * heads * head_dim elements on CUDA device `index`."""
+    if t.dtype is not _bf16() or t.numel() != rows * heads * head_dim or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{what}: expected contiguous bfloat16 [{rows}, {heads}, {head_dim}] on cuda:{index}")
     return t.data_ptr()
 
 
-def _on(device):
+def _bf16():
+    global _bf16
     import torch
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}: make it the current device for the call")
+    bf16 = torch.bfloat16
+    _bf16 = lambda: bf16  # noqa: E731
+    return bf16
 
 
-def _flag(err_flag, device):
+def _launch_on(index: int, stream) -> int:
+    """The stream handle of a call on CUDA device `index`, which has to be the current one."""
+    global _launch_on
     import torch
+    current, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+    def launch_on(index: int, stream) -> int:
+        if current() != index:
+            raise ValueError(f"tensors on cuda:{index}: make it the current device for the call")
+        return raw(index) if stream is None else stream.cuda_stream
+
+    _launch_on = launch_on
+    return launch_on(index, stream)
+
+
+def _flag(err_flag, index):
     if err_flag is None:
         return None
-    if err_flag.dtype is not torch.int32 or err_flag.device != device:
-        raise ValueError(f"err_flag: expected int32 on {device}")
+    import torch
+    if err_flag.dtype is not torch.int32 or err_flag.get_device() != index:
+        raise ValueError(f"err_flag: expected int32 on cuda:{index}")
     return err_flag.data_ptr()
 
 
@@ -639,39 +660,45 @@ def tern_qk_norm_rope(spec: QkvSpec, src, pos, q, k, flags: int = 0, stream=None
     """Norm and rotation of the q and k heads of src [rows, >= (q_heads + kv_heads) * head_dim] (fp32 or
     bf16) at positions pos (int32 [rows]) into bf16 q [rows, q_heads, head_dim] and k [rows, kv_heads,
     head_dim]."""
-    import torch
-    _on(spec.device)
-    rows, D = src.shape[0], spec.head_dim
-    _want(pos, "pos", (torch.int32,), (rows,), spec.device)
-    c = spec._at(src, 1)
-    _check(lib().tern_qk_norm_rope(ctypes.byref(c), rows, pos.data_ptr(), _heads_out(q, "q", rows, spec.q_heads, D, spec.device),
-                                   _heads_out(k, "k", rows, spec.kv_heads, D, spec.device), flags, _stream(stream)),
-           "tern_qk_norm_rope")
+    index, D = spec.index, spec.head_dim
+    st = _launch_on(index, stream)
+    c, rows = spec._at(src, 1)
+    if pos.dtype is not spec.i32 or pos.numel() != rows or not pos.is_contiguous() or pos.get_device() != index:
+        raise ValueError(f"pos: expected contiguous int32 [{rows}] on cuda:{index}")
+    status = lib().tern_qk_norm_rope(ctypes.byref(c), rows, pos.data_ptr(), _heads_out(q, "q", rows, spec.q_heads, D, index),
+                                     _heads_out(k, "k", rows, spec.kv_heads, D, index), flags, st)
+    if status:
+        _check(status, "tern_qk_norm_rope")
 
 
 def tern_kv_append(spec: QkvSpec, src, cache: KvCache, batch: KvBatch, q, err_flag=None, flags: int = 0, stream=None) -> None:
     """Append the keys and values of src [rows, >= (q_heads + 2 kv_heads) * head_dim] (fp32 or bf16) to the
     cache and write the rows' queries to q, bf16 [rows, q_heads, head_dim]. err_flag: optional int32
     tensor, set nonzero for sequences or pages the call has to leave out (never cleared here)."""
-    _on(spec.device)
-    if cache.device != spec.device or batch.device != spec.device:
+    index = spec.index
+    st = _launch_on(index, stream)
+    if cache.index != index or batch.index != index:
         raise ValueError("spec, cache and batch on different devices")
-    if src.shape[0] != batch.rows:
-        raise ValueError(f"src: {src.shape[0]} rows, the batch has {batch.rows}")
-    c = spec._at(src, 2)
-    _check(lib().tern_kv_append(ctypes.byref(c), cache._ref, batch._ref,
-                                _heads_out(q, "q", batch.rows, spec.q_heads, spec.head_dim, spec.device),
-                                _flag(err_flag, spec.device), flags, _stream(stream)), "tern_kv_append")
+    c, rows = spec._at(src, 2)
+    if rows != batch.rows:
+        raise ValueError(f"src: {rows} rows, the batch has {batch.rows}")
+    status = lib().tern_kv_append(ctypes.byref(c), cache._ref, batch._ref,
+                                  _heads_out(q, "q", rows, spec.q_heads, spec.head_dim, index),
+                                  _flag(err_flag, index), flags, st)
+    if status:
+        _check(status, "tern_kv_append")
 
 
 def tern_kv_read(cache: KvCache, batch: KvBatch, k, v, err_flag=None, stream=None) -> None:
     """The rows' tokens out of the cache: bf16 k and v [rows, kv_heads, head_dim]."""
-    _on(cache.device)
-    if batch.device != cache.device:
+    index, rows, heads, D = cache.index, batch.rows, cache.kv_heads, cache.head_dim
+    st = _launch_on(index, stream)
+    if batch.index != index:
         raise ValueError("cache and batch on different devices")
-    _check(lib().tern_kv_read(cache._ref, batch._ref, _heads_out(k, "k", batch.rows, cache.kv_heads, cache.head_dim, cache.device),
-                              _heads_out(v, "v", batch.rows, cache.kv_heads, cache.head_dim, cache.device),
-                              _flag(err_flag, cache.device), _stream(stream)), "tern_kv_read")
+    status = lib().tern_kv_read(cache._ref, batch._ref, _heads_out(k, "k", rows, heads, D, index),
+                                _heads_out(v, "v", rows, heads, D, index), _flag(err_flag, index), st)
+    if status:
+        _check(status, "tern_kv_read")
 
 
 def tern_paged_attn_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -684,17 +711,19 @@ def tern_paged_attn(q, scale: float, cache: KvCache, batch: KvBatch, out, worksp
     if given, fp32 lse [rows, q_heads]. workspace: a zero-filled uint8 CUDA tensor of at least
     tern_paged_attn_workspace_bytes(...) bytes, one per stream of calls. max_rows: the largest number of
     rows a sequence is expected to bring (any value is right; it picks the kernel)."""
-    import torch
-    _on(cache.device)
-    if batch.device != cache.device or workspace.device != cache.device:
-        raise ValueError("cache, batch and workspace on different devices")
+    index, rows, D = cache.index, batch.rows, cache.head_dim
+    st = _launch_on(index, stream)
+    if batch.index != index or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("cache, batch and workspace on different devices, or a strided workspace")
     if q.dim() != 3:
         raise ValueError("q: expected bfloat16 [rows, q_heads, head_dim]")
     Hq = q.shape[1]
-    if lse is not None and (lse.dtype is not torch.float32 or lse.device != cache.device or not lse.is_contiguous()
-                            or lse.numel() != batch.rows * Hq):
-        raise ValueError(f"lse: expected contiguous float32 [{batch.rows}, {Hq}] on {cache.device}")
-    _check(lib().tern_paged_attn(_heads_out(q, "q", batch.rows, Hq, cache.head_dim, cache.device), Hq, scale, cache._ref,
-                                 batch._ref, max_rows, _heads_out(out, "out", batch.rows, Hq, cache.head_dim, cache.device),
-                                 _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 _flag(err_flag, cache.device), flags, _stream(stream)), "tern_paged_attn")
+    if lse is not None:
+        if lse.dtype is not cache.f32 or lse.numel() != rows * Hq or not lse.is_contiguous() or lse.get_device() != index:
+            raise ValueError(f"lse: expected contiguous float32 [{rows}, {Hq}] on cuda:{index}")
+        lse = lse.data_ptr()
+    status = lib().tern_paged_attn(_heads_out(q, "q", rows, Hq, D, index), Hq, scale, cache._ref, batch._ref, max_rows,
+                                   _heads_out(out, "out", rows, Hq, D, index), lse, workspace.data_ptr(), workspace.nbytes,
+                                   _flag(err_flag, index), flags, st)
+    if status:
+        _check(status, "tern_paged_attn")

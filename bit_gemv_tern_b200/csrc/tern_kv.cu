@@ -79,7 +79,7 @@ __device__ __forceinline__ void norm_rope(Halves<D / 64>& h, const Halves<D / 64
 #pragma unroll
     for (int e = 0; e < V; ++e) ss += h.lo[e] * h.lo[e] + h.hi[e] * h.hi[e];
     ss = warp_sum<V>(ss);
-    r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+    r = rsqrtf(ss * (1.0f / D) + eps);
   }
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -109,16 +109,21 @@ __device__ __forceinline__ Halves<D / 64> load_gain(const uint16_t* gain, int la
   return Halves<D / 64>{};
 }
 
+__device__ __forceinline__ int code_of(float x, float inv) {
+  const int c = __float2int_rn(x * inv);
+  return max(-127, min(127, c));
+}
+
 // The codes of one token in one block: a lane's 2V codes leave as one store, after neighbours have
 // traded halves (the even lane writes the first half's, the odd lane the second half's).
 template <int D>
-__device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 64>& h, float s, int lane) {
+__device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 64>& h, float inv, int lane) {
   constexpr int V = D / 64;
   uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    lo |= (uint32_t)(quant_i8(h.lo[e], s) & 0xFF) << (8 * e);
-    hi |= (uint32_t)(quant_i8(h.hi[e], s) & 0xFF) << (8 * e);
+    lo |= (uint32_t)(code_of(h.lo[e], inv) & 0xFF) << (8 * e);
+    hi |= (uint32_t)(code_of(h.hi[e], inv) & 0xFF) << (8 * e);
   }
   const bool odd = lane & 1;
   const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
@@ -159,6 +164,7 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const float s = fmaxf(fmaxf(old, __fdiv_rn(top, 127.0f)), kKvScaleFloor);
+  const float inv = __fdiv_rn(1.0f, s);
   if (first && s != old) {
     // the block's scale grows: its earlier codes move to the new one (D/32 bytes of a token per lane)
     const float f = __fdiv_rn(old, s);
@@ -170,7 +176,7 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
   }
 #pragma unroll
   for (int j = 0; j < TERN_KV_BLOCK; ++j)
-    if (j < cnt) store_codes<D>(codes + (first + j) * D, x[j], s, lane);
+    if (j < cnt) store_codes<D>(codes + (first + j) * D, x[j], inv, lane);
   if (lane == 0 && s != old) *scale = s;
 }
 
@@ -240,37 +246,53 @@ __global__ void __launch_bounds__(kQkvThreads) k_qkv(const __grid_constant__ Qkv
   }
 }
 
-// Eight elements of one token and head per thread and step: 8 code bytes in, 16 bytes out.
+// Sixteen elements of one token and head per thread and step: 16 code bytes in, 32 bytes out. Where a row's token
+// lies is looked up once per row; the rows of a CTA are few where there are few in all.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadParams p) {
   __shared__ int seq[kReadWindow];
+  __shared__ int at[kReadWindow][2];              // page (-1: none), place
   const KvView& kv = p.kv;
-  const int w0 = blockIdx.x * kReadWindow, wn = min(kReadWindow, kv.rows - w0);
+  const int w0 = blockIdx.x * p.window, wn = min(p.window, kv.rows - w0);
   locate_rows<256>(kv, w0, wn, true, seq);
-  const int per_row = kv.kv_heads * (D / 8);
-  for (int t = threadIdx.x; t < wn * per_row * 2; t += 256) {
-    const bool is_v = t >= wn * per_row;
-    const int u = is_v ? t - wn * per_row : t;
-    const int i = u / per_row, hk = u % per_row / (D / 8), c = u % (D / 8), b = seq[i], row = w0 + i;
-    if (b < 0) continue;
-    const int pos = __ldg(kv.kv_len + b) - (__ldg(kv.row_start + b + 1) - row);
-    const int page = __ldg(kv.table + (int64_t)b * kv.max_pages + pos / kv.page_size);
-    if (page < 0 || page >= kv.pages) {
-      if (kv.flag) *kv.flag = 1;
-      continue;
+  if (threadIdx.x < wn) {
+    const int b = seq[threadIdx.x], row = w0 + threadIdx.x;
+    int page = -1, place = 0;
+    if (b >= 0) {
+      const int pos = __ldg(kv.kv_len + b) - (__ldg(kv.row_start + b + 1) - row);
+      page = __ldg(kv.table + (int64_t)b * kv.max_pages + pos / kv.page_size);
+      place = pos % kv.page_size;
+      if (page < 0 || page >= kv.pages) {
+        page = -1;
+        if (kv.flag) *kv.flag = 1;
+      }
     }
-    const int place = pos % kv.page_size;
+    at[threadIdx.x][0] = page;
+    at[threadIdx.x][1] = place;
+  }
+  __syncthreads();
+  const int per_row = kv.kv_heads * (D / 16), all = wn * per_row;
+#pragma unroll 2
+  for (int t = threadIdx.x; t < 2 * all; t += 256) {
+    const bool is_v = t >= all;
+    const int u = is_v ? t - all : t;
+    const int i = u / per_row, r = u - i * per_row, hk = r / (D / 16), c = r % (D / 16);
+    const int page = at[i][0], place = at[i][1];
+    if (page < 0) continue;
     const int64_t head = (int64_t)page * kv.kv_heads + hk;
-    const float s = (is_v ? kv.vs : kv.ks)[head * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK];
-    const uint2 w = *reinterpret_cast<const uint2*>((is_v ? kv.v : kv.k) + (head * kv.page_size + place) * D + c * 8);
-    uint32_t o[4];
+    const float s = __ldg((is_v ? kv.vs : kv.ks) + head * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK);
+    const uint4 w = ld_nc((is_v ? kv.v : kv.k) + (head * kv.page_size + place) * D + c * 16);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t x = (e < 2 ? w.x : w.y) >> (16 * (e & 1));
-      const __nv_bfloat162 v = __floats2bfloat162_rn((float)(int8_t)(x & 0xFF) * s, (float)(int8_t)((x >> 8) & 0xFF) * s);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t y = x[e >> 1] >> (16 * (e & 1));
+      const __nv_bfloat162 v = __floats2bfloat162_rn((float)(int8_t)(y & 0xFF) * s, (float)(int8_t)((y >> 8) & 0xFF) * s);
       o[e] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    *reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((int64_t)row * kv.kv_heads + hk) * D + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + ((int64_t)(w0 + i) * kv.kv_heads + hk) * D + c * 16);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -282,9 +304,12 @@ cudaError_t launch_qkv_t(const QkvParams& p, bool pdl, cudaStream_t st) {
   const int windows = wide ? (p.rows + kWindow - 1) / kWindow : p.rows;
   const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
   const int warps = kQkvThreads / 32;
-  // split the heads over CTAs until every SM has two
-  int split = (2 * device_sm_count() + windows - 1) / windows;
+  // split the heads over CTAs until every SM has eight: a warp then takes one head or a few
+  int split = (8 * device_sm_count() + windows - 1) / windows;
   if (split > (tasks + warps - 1) / warps) split = (tasks + warps - 1) / warps;
+  // the fewest CTAs with as many rounds of heads
+  const int rounds = (tasks + split * warps - 1) / (split * warps);
+  split = (tasks + rounds * warps - 1) / (rounds * warps);
   const dim3 grid(windows, split);
   return wide ? launch_maybe_pdl(k_qkv<D, BF16, APPEND, kWindow>, grid, dim3(kQkvThreads), 0, pdl, st, p)
               : launch_maybe_pdl(k_qkv<D, BF16, APPEND, 1>, grid, dim3(kQkvThreads), 0, pdl, st, p);
@@ -301,8 +326,11 @@ cudaError_t launch_qkv(const QkvParams& p, int head_dim, bool bf16, bool append,
   return bf16 ? launch_qkv_t<64, true, false>(p, pdl, st) : launch_qkv_t<64, false, false>(p, pdl, st);
 }
 
-cudaError_t launch_kv_read(const KvReadParams& p, int head_dim, cudaStream_t st) {
-  const int grid = (p.kv.rows + kReadWindow - 1) / kReadWindow;
+cudaError_t launch_kv_read(KvReadParams& p, int head_dim, cudaStream_t st) {
+  // windows of 16 rows, fewer while the SMs would have less than two CTAs each
+  p.window = p.kv.rows / (2 * device_sm_count());
+  p.window = p.window < 1 ? 1 : p.window > kReadWindow ? kReadWindow : p.window;
+  const int grid = (p.kv.rows + p.window - 1) / p.window;
   if (head_dim == 128) k_kv_read<128><<<grid, 256, 0, st>>>(p);
   else k_kv_read<64><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();

@@ -63,8 +63,9 @@ struct KvReadParams {
   KvView kv;
   uint16_t* k;
   uint16_t* v;
+  int32_t window;              // rows of a CTA, set by the launch
 };
-cudaError_t launch_kv_read(const KvReadParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_kv_read(KvReadParams& p, int head_dim, cudaStream_t st);
 
 struct AttnParams {
   KvView kv;

@@ -606,7 +606,7 @@ tern_status tern_qk_norm_rope(const tern_qkv* x, int32_t rows, const int32_t* po
  *   s = max(s_old, absmax of its new values / 127, 2^-60)
  * where s_old is the block's scale if it holds earlier tokens of the sequence, else 0 (what lies in a
  * fresh block is not looked at); where s grows, the earlier codes become rint(code * (s_old / s)).
- * New codes are clamp(rint(value / s), -127, 127). Appending the same rows at the same place
+ * New codes are clamp(rint(value * (1 / s)), -127, 127), in fp32. Appending the same rows at the same place
  * again leaves the cache as it is, so a call may be repeated, and after a rejected draft the
  * next call simply comes with a smaller kv_len.
  * flags: 0 or TERN_FLAG_PDL (the kernel waits for the preceding one before it reads anything). */

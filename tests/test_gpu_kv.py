@@ -126,7 +126,7 @@ def run_append(P, spec, g, dtype, seed, stride=None):
     end = P.row_start[-1]
     pos = np.concatenate([np.arange(kv - n, kv) for n, kv in P.lens]) if end else np.zeros(0)
     if end:
-        close_bf16(host(q)[:end], *norm_rope(x[:end, :P.q_heads], g[0], pos, spec.freq.cpu().numpy(), spec._c.eps))
+        close_bf16(host(q)[:end], *norm_rope(x[:end, :P.q_heads], g[0], pos, spec.freq.cpu().numpy(), spec.eps))
     assert (host(q)[end:] == 7.0).all()
     check_append(P, spec, g, x, before, after)
     tg.tern_kv_append(spec, src, cache, batch, q, flag)               # the same rows at the same place

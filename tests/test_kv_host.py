@@ -134,8 +134,8 @@ def test_python_binding_refuses_other_tensors(tg):
                  lambda: tg._want(codes, "k", (torch.int8,), (2, 1, 16, 64)),
                  lambda: tg._want(codes.transpose(0, 2), "k", (torch.int8,)),
                  lambda: tg._want(codes, "k", (torch.int8,), device=torch.device("cuda", 0)),
-                 lambda: tg._heads_out(torch.zeros(4, 2, 128), "q", 4, 2, 128, torch.device("cpu")),
-                 lambda: tg._heads_out(torch.zeros(4, 2, 128, dtype=torch.bfloat16), "q", 5, 2, 128, torch.device("cpu")),
-                 lambda: tg._flag(torch.zeros(1), torch.device("cpu"))):
+                 lambda: tg._heads_out(torch.zeros(4, 2, 128), "q", 4, 2, 128, -1),
+                 lambda: tg._heads_out(torch.zeros(4, 2, 128, dtype=torch.bfloat16), "q", 5, 2, 128, -1),
+                 lambda: tg._flag(torch.zeros(1), -1)):
         with pytest.raises(ValueError):
             call()
