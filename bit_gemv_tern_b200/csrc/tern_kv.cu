@@ -181,15 +181,28 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
 }
 
 template <int D, bool BF16, bool APPEND, int W>
-__global__ void __launch_bounds__(kQkvThreads) k_qkv(const __grid_constant__ QkvParams p) {
+__global__ void __launch_bounds__(kQkvThreads, APPEND ? 2 : 4) k_qkv(const __grid_constant__ QkvParams p) {
   constexpr int V = D / 64;
   __shared__ float2 tab[kWindow][D / 2];
   __shared__ int seq[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w0 = blockIdx.x * W, wn = min(W, p.rows - w0);
   const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
+  // source head of a warp's task: keys and values first (they take longest), then queries
+  auto source_head = [&](int t) {
+    if (!APPEND) return t;
+    return t < 2 * p.kv_heads ? p.q_heads + t : t - 2 * p.kv_heads;
+  };
+  const int t0 = blockIdx.y * (kQkvThreads / 32) + warp;
   pdl_wait();
   pdl_launch_dependents();
+  // the rows of the warp's first head are on their way while the sequences are looked up and the angles computed
+  if (t0 < tasks) {
+    constexpr int kLines = D * (BF16 ? 2 : 4) / 128;
+    const char* src = static_cast<const char*>(p.src) + (int64_t)source_head(t0) * D * (BF16 ? 2 : 4);
+    for (int l = lane; l < wn * kLines; l += 32)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(src + (int64_t)(w0 + l / kLines) * p.stride * (BF16 ? 2 : 4) + l % kLines * 128));
+  }
   if constexpr (APPEND) locate_rows<kQkvThreads>(p.kv, w0, wn, true, seq);
   for (int i = 0; i < wn; i += APPEND ? 1 : W) {
     int row = w0 + i, cnt = wn, pos0 = 0, b = 0;
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kQkvThreads) k_qkv(const __grid_constant__ Qkv
         page = -1;
       }
     }
-    for (int t = blockIdx.y * (kQkvThreads / 32) + warp; t < tasks; t += gridDim.y * (kQkvThreads / 32)) {
+    for (int t = t0; t < tasks; t += gridDim.y * (kQkvThreads / 32)) {
       if constexpr (APPEND) {
         if (t < 2 * p.kv_heads) {
           if (page >= 0)
