@@ -63,13 +63,13 @@ struct Shape {
   // 2t + 1 go out as 16-byte stores without bank conflicts
   static constexpr int kRowPitch = D == 128 ? 148 : 84;
   static __device__ __forceinline__ int place(int d) { return D == 128 ? d + 4 * (((d >> 4) + 1) >> 1) : d + 4 * (d >> 4); }
-  // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][2][4] | masks | barriers
+  // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][block][4] | masks | barriers
   static constexpr int kOffJoin = kStages * 2 * kHalfStage;
   static constexpr int kOffMax = kOffJoin + kCW * R * kRowPitch * 4;
   static constexpr int kOffSum = kOffMax + kCW * R * 4;
   static constexpr int kOffScale = kOffSum + kCW * R * 4;
-  static constexpr int kOffMask = kOffScale + kStages * 2 * kBlocks * 4;
-  static constexpr int kOffQ = kOffMask + kStages * 4;            // R = 32: query fragments [step][NT][32] x 8 B
+  static constexpr int kOffMask = kOffScale + kStages * 4 * kBlocks * 4;
+  static constexpr int kOffQ = kOffMask + kStages * 4;            // R = 32: query fragments [step][NT / 2][32] x 16 B
   static constexpr int kOffBar = kOffQ + (R == 32 ? D / 16 * kNT * 256 : 0);
   static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
@@ -203,9 +203,8 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
             }
           smask[s] = have;
         }
-        const int from = at * kBlocks + (lane & (kBlocks - 1));
-        const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, from), vs = __shfl_sync(0xFFFFFFFFu, cur.vs, from);
-        if (lane < 2 * kBlocks) sscale[s * 2 * kBlocks + lane] = lane < kBlocks ? ks : vs;
+        if (lane / kBlocks == at)                // ks, log2 vs, 1 / vs of the chunk's blocks
+          *reinterpret_cast<float4*>(sscale + (s * kBlocks + lane % kBlocks) * 4) = make_float4(cur.ks, __log2f(cur.vs), __fdividef(1.0f, cur.vs), 0.0f);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
         if (++at == kAhead) at = 0;
@@ -262,13 +261,13 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
           if constexpr (R == 32) {
             // step 2i + e/2 of the fragments in shared memory; every warp writes the same
             uint32_t* sq = reinterpret_cast<uint32_t*>(sm + SH::kOffQ);
-            if (warp == n) sq[(((2 * i + (e >> 1)) * NT + n) * 32 + lane) * 2 + (e & 1)] = h;
+            if (warp == n) sq[(((2 * i + (e >> 1)) * (NT / 2) + n / 2) * 32 + lane) * 4 + (n & 1) * 2 + (e & 1)] = h;
           } else {
             qf[n][2 * i + (e >> 1)][e & 1] = h;
           }
         }
       }
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kNoMax;
       l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < T; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
@@ -285,7 +284,8 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * s, (qs / ST) & 1));
       if (ok && t0 < w.vis && (smask[s] >> j & 1)) {
         const uint32_t kb = base + s * 2 * SH::kHalfStage + j * TERN_KV_BLOCK * D, vb = kb + SH::kHalfStage;
-        const float ks = sscale[s * 2 * kBlocks + j], vs = sscale[s * 2 * kBlocks + kBlocks + j];
+        const float4 sc = *reinterpret_cast<const float4*>(sscale + (s * kBlocks + j) * 4);
+        const float ks = sc.x, lv = sc.y, iv = sc.z;
         // keys: tokens g and g + 8, elements t * D/4 .. of the head
         float c[NT][4];
 #pragma unroll
@@ -300,20 +300,21 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
           for (int e = 0; e < 4; ++e) {
             const uint32_t a0 = codes_f16<0x4140>(xs[e]), a2 = codes_f16<0x4342>(xs[e]);
             const uint32_t a1 = codes_f16<0x4140>(ys[e]), a3 = codes_f16<0x4342>(ys[e]);
+            if constexpr (R == 32) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if constexpr (R == 32) {
-                const uint2 b = lds64(base + SH::kOffQ + (((4 * h + e) * NT + n) * 32 + lane) * 8);
+              for (int n = 0; n < NT; n += 2) {
+                const uint4 b = lds128(base + SH::kOffQ + (((4 * h + e) * (NT / 2) + n / 2) * 32 + lane) * 16);
                 mma_f16(c[n], a0, a1, a2, a3, b.x, b.y);
-              } else {
-                mma_f16(c[n], a0, a1, a2, a3, qf[n][4 * h + e][0], qf[n][4 * h + e][1]);
+                mma_f16(c[n + 1], a0, a1, a2, a3, b.z, b.w);
               }
+            } else {
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(c[n], a0, a1, a2, a3, qf[n][4 * h + e][0], qf[n][4 * h + e][1]);
             }
           }
         }
-        const float lv = __log2f(vs), iv = __fdividef(1.0f, vs);
         const bool edge = t0 + TERN_KV_BLOCK > clear;
-        uint32_t pb[NT][2];
+        bool rise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float f0 = rowf[n][0] * ks, f1 = rowf[n][1] * ks;
@@ -329,18 +330,23 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
             if (t0 + g + 8 > p0) c[n][2] = -INFINITY;
             if (t0 + g + 8 > p1) c[n][3] = -INFINITY;
           }
-          float x0 = fmaxf(c[n][0], c[n][2]), x1 = fmaxf(c[n][1], c[n][3]);
+          rise |= fmaxf(c[n][0], c[n][2]) > m[n][0] + kSlack || fmaxf(c[n][1], c[n][3]) > m[n][1] + kSlack;
+        }
+        // only where some row's maximum rises by more than the slack are the lanes' maxima joined and the sums rescaled
+        if (__any_sync(0xFFFFFFFFu, rise)) {
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, d));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, d));
-          }
-          const bool rise = x0 > m[n][0] + kSlack || x1 > m[n][1] + kSlack;
-          if (__any_sync(0xFFFFFFFFu, rise)) {
-            const float n0 = fmaxf(m[n][0], x0), n1 = fmaxf(m[n][1], x1);
-            const float r0 = n0 == -INFINITY ? 1.0f : exp2_approx(m[n][0] - n0), r1 = n1 == -INFINITY ? 1.0f : exp2_approx(m[n][1] - n1);
-            m[n][0] = n0;
-            m[n][1] = n1;
+          for (int n = 0; n < NT; ++n) {
+            float x0 = fmaxf(c[n][0], c[n][2]), x1 = fmaxf(c[n][1], c[n][3]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, d));
+              x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, d));
+            }
+            x0 = fmaxf(m[n][0], x0);
+            x1 = fmaxf(m[n][1], x1);
+            const float r0 = exp2_approx(m[n][0] - x0), r1 = exp2_approx(m[n][1] - x1);
+            m[n][0] = x0;
+            m[n][1] = x1;
             l[n][0] *= r0;
             l[n][1] *= r1;
 #pragma unroll
@@ -351,9 +357,12 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
               o[k][n][3] *= r1;
             }
           }
-          const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-          const float e0 = exp2_approx(c[n][0] - m0), e1 = exp2_approx(c[n][1] - m1);
-          const float e2 = exp2_approx(c[n][2] - m0), e3 = exp2_approx(c[n][3] - m1);
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float e0 = exp2_approx(c[n][0] - m[n][0]), e1 = exp2_approx(c[n][1] - m[n][1]);
+          const float e2 = exp2_approx(c[n][2] - m[n][0]), e3 = exp2_approx(c[n][3] - m[n][1]);
           l[n][0] = fmaf(e0 + e2, iv, l[n][0]);
           l[n][1] = fmaf(e1 + e3, iv, l[n][1]);
           pb[n][0] = movmatrix_trans(pack_f16(e0, e1));
@@ -406,13 +415,13 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     named_sync(1, CW * 32);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float n0 = -INFINITY, n1 = -INFINITY;
+      float n0 = kNoMax, n1 = kNoMax;
 #pragma unroll
       for (int x = 0; x < CW; ++x) {
         n0 = fmaxf(n0, smax[x * R + 8 * n + 2 * t]);
         n1 = fmaxf(n1, smax[x * R + 8 * n + 2 * t + 1]);
       }
-      const float f0 = m[n][0] == -INFINITY ? 0.0f : exp2_approx(m[n][0] - n0), f1 = m[n][1] == -INFINITY ? 0.0f : exp2_approx(m[n][1] - n1);
+      const float f0 = exp2_approx(m[n][0] - n0), f1 = exp2_approx(m[n][1] - n1);
       if (g == 0) {
         ssum[warp * R + 8 * n + 2 * t] = l[n][0] * f0;
         ssum[warp * R + 8 * n + 2 * t + 1] = l[n][1] * f1;
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     for (int x = warp * 32 + lane; x < rows * (D / 4); x += CW * 32) {
       const int r = x / (D / 4), d = x % (D / 4) * 4;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float sum = 0.0f, top = -INFINITY;
+      float sum = 0.0f, top = kNoMax;
 #pragma unroll
       for (int y = 0; y < CW; ++y) {
         if ((y - phase + CW) % CW < used) {
@@ -482,19 +491,19 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
           const int c = c0 + x / R;
           const float* y = parts + (int64_t)(2 * c + (c == c0)) * SH::kPartFloats + R * D + x % R;
           const bool have = x % R < rows;
-          pm[x] = have ? __ldcg(y) : -INFINITY;
+          pm[x] = have ? __ldcg(y) : kNoMax;
           pl[x] = have ? __ldcg(y + R) : 0.0f;
         }
         named_sync(1, CW * 32);
         for (int x = warp * 32 + lane; x < rows * (D / 4); x += CW * 32) {
           const int r = x / (D / 4), d = x % (D / 4) * 4;
-          float top = -INFINITY;
+          float top = kNoMax;
           for (int i = 0; i < np; ++i) top = fmaxf(top, pm[i * R + r]);
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float sum = 0.0f;
 #pragma unroll 8
           for (int i = 0; i < np; ++i) {
-            const float mt = pm[i * R + r], f = mt == -INFINITY ? 0.0f : exp2_approx(mt - top);
+            const float f = exp2_approx(pm[i * R + r] - top);
             const float4 u = __ldcg(reinterpret_cast<const float4*>(parts + (int64_t)(2 * (c0 + i) + (i == 0)) * SH::kPartFloats + r * D + d));
             v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
             sum = fmaf(pl[i * R + r], f, sum);

@@ -20,6 +20,8 @@ constexpr int kCounterBytes = 8192;               // the workspace's counters, b
 // The running maximum follows only when it rises by more than this (a power of two of slack in p'
 // instead of a rescale of the output for every small rise).
 constexpr float kSlack = 8.0f;
+// The maximum of no token at all: finite, so that differences of it with itself and with minus infinity are not nan.
+constexpr float kNoMax = -1e30f;
 
 
 struct alignas(64) AttnMaps {
