@@ -49,11 +49,12 @@ constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
 constexpr int kTileCost = 4;
 template <int D, int R>
 struct Shape {
-  // CTAs on an SM: while one joins its warps at the end of a tile, the other's stream goes on. 16, 12 or 8 warps
-  // on the SM in all, four, three or two to a register file partition: 128, 168 or 255 registers a thread.
+  // CTAs on an SM: while one joins its warps at the end of a tile, the other's stream goes on. 12 warps on the SM, three to
+  // a register file partition (168 registers a thread), for 32 rows 8 (255 registers); 16 warps with 128 registers were
+  // 2% slower for 8 rows.
   static constexpr int kPerSM = R == 32 ? 1 : 2;
   static constexpr int kProducers = R == 32 ? 2 : 1;
-  static constexpr int kCW = (R == 8 ? 16 : R == 16 ? 12 : 8) / kPerSM - kProducers;   // consumer warps
+  static constexpr int kCW = (R == 32 ? 8 : 12) / kPerSM - kProducers;   // consumer warps
   static constexpr int kThreads = (kCW + kProducers) * 32;
   static constexpr int kNT = R / 8;                               // 8-row column groups
   static constexpr int kTiles = D / 16;                           // 16-element tiles of a head

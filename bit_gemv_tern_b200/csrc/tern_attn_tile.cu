@@ -456,15 +456,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
         if (!wait(k_full + 8 * (n & 1), n >> 1) || !wait(q_full + 8 * q, tiles++) || (nq && !wait(pv_done + 8 * q, nq - 1))) break;
         scores(n & 1);
         for (int c = 0; c < seg; ++c, ++n, ++nq) {
-          if (!wait(v_full + 8 * (n & 1), n >> 1) || !wait(p_full + 16 * q, nq)) break;
+          const bool next = c + 1 < seg;
+          if (!wait(v_full + 8 * (n & 1), n >> 1) || (next && !wait(k_full + 8 * ((n + 1) & 1), (n + 1) >> 1))) break;
+          if (!wait(p_full + 16 * q, nq)) break;
           product(0, n & 1, c > 0);
           if (!wait(p_full + 16 * q + 8, nq)) break;
           product(1, n & 1, true);
-          if (c + 1 < seg) {
-            // the next scores go over P once that has been read
-            if (!wait(k_full + 8 * ((n + 1) & 1), (n + 1) >> 1) || !wait(pv_done + 8 * q, nq)) break;
-            scores((n + 1) & 1);
-          }
+          // the next scores go over P once that has been read
+          if (next && !wait(pv_done + 8 * q, nq)) break;
+          if (next) scores((n + 1) & 1);
         }
       }
       // every MMA issued has completed once done_bar flips
