@@ -44,6 +44,7 @@ namespace {
 
 constexpr int kChunk = 64;                        // tokens of a stage: four blocks
 constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
+constexpr uint32_t kMaxPolls = 1u << 26;          // seconds, then a wait for a stage gives up
 // What a tile costs beside its chunks (queries in, warps joined, result out), in chunks: measured 2.5 us of a
 // CTA that streams a chunk in 0.7 us.
 constexpr int kTileCost = 4;
@@ -64,13 +65,13 @@ struct Shape {
   // 2t + 1 go out as 16-byte stores without bank conflicts
   static constexpr int kRowPitch = D == 128 ? 148 : 84;
   static __device__ __forceinline__ int place(int d) { return D == 128 ? d + 4 * (((d >> 4) + 1) >> 1) : d + 4 * (d >> 4); }
-  // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][block][4] | masks | barriers
+  // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][block][4] | masks, stage numbers | barriers
   static constexpr int kOffJoin = kStages * 2 * kHalfStage;
   static constexpr int kOffMax = kOffJoin + kCW * R * kRowPitch * 4;
   static constexpr int kOffSum = kOffMax + kCW * R * 4;
   static constexpr int kOffScale = kOffSum + kCW * R * 4;
   static constexpr int kOffMask = kOffScale + kStages * 4 * kBlocks * 4;
-  static constexpr int kOffQ = kOffMask + kStages * 4;            // R = 32: query fragments [step][NT / 2][32] x 16 B
+  static constexpr int kOffQ = kOffMask + kStages * 8;            // R = 32: query fragments [step][NT / 2][32] x 16 B
   static constexpr int kOffBar = kOffQ + (R == 32 ? D / 16 * kNT * 256 : 0);
   static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   float* ssum = reinterpret_cast<float*>(sm + SH::kOffSum);
   float* sscale = reinterpret_cast<float*>(sm + SH::kOffScale);
   uint32_t* smask = reinterpret_cast<uint32_t*>(sm + SH::kOffMask);
+  int* sstage = reinterpret_cast<int*>(smask + ST);                  // the stage a slot holds or is being filled with
   const uint32_t full = base + SH::kOffBar, empty = full + 8 * ST;
   __shared__ Plan plan;
   __shared__ longlong2 warp_sums[SH::kThreads / 32];
@@ -112,6 +114,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     for (int s = 0; s < ST; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, kBlocks);
+      sstage[s] = -1;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
               bytes += 2 * p.box * D;
             }
           smask[s] = have;
+          *reinterpret_cast<volatile int*>(&sstage[s]) = q;
         }
         if (lane / kBlocks == at)                // ks, log2 vs, 1 / vs of the chunk's blocks
           *reinterpret_cast<float4*>(sscale + (s * kBlocks + lane % kBlocks) * 4) = make_float4(cur.ks, __log2f(cur.vs), __fdividef(1.0f, cur.vs), 0.0f);
@@ -282,7 +286,13 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     for (int i = turn; i < seg * kBlocks; i += CW) {
       const int qs = q0 + i / kBlocks, s = qs % ST, j = i % kBlocks;
       const int t0 = (off + i / kBlocks) * kChunk + j * TERN_KV_BLOCK;
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * s, (qs / ST) & 1));
+      // A wait tells the phases of a slot apart by parity alone, and a warp may skip stages, so that a slot whose last but
+      // one stage is late would look like this one: the slot has to hold this stage before its phase means anything.
+      if (ok) {
+        uint32_t polls = 0;
+        while (*reinterpret_cast<volatile int*>(&sstage[s]) != qs && ++polls < kMaxPolls) {}
+        ok = __all_sync(0xFFFFFFFFu, polls < kMaxPolls && mbar_wait(full + 8 * s, (qs / ST) & 1));
+      }
       if (ok && t0 < w.vis && (smask[s] >> j & 1)) {
         const uint32_t kb = base + s * 2 * SH::kHalfStage + j * TERN_KV_BLOCK * D, vb = kb + SH::kHalfStage;
         const float4 sc = *reinterpret_cast<const float4*>(sscale + (s * kBlocks + j) * 4);

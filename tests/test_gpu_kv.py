@@ -305,6 +305,25 @@ def test_attention_over_a_long_cache_and_again():
     run_attn(Paged(73, heads, 16, [(1, 3000)]), 74, ws=ws)
 
 
+@pytest.mark.parametrize("lens,max_rows", [([(1, 30_000), (1, 900)], 1), ([(4, 12_000)], 4), ([(8, 12_000)], 8), ([(200, 6000)], 200)])
+def test_attention_gives_the_same_bits_whether_its_cache_is_cold_or_not(lens, max_rows):
+    """Stages that arrive late and out of order (pages scattered over memory, the L2 flushed) change nothing."""
+    P = Paged(75, H8B, 64, lens)
+    cache, batch = P.device(tg)
+    q = torch.randn(P.rows, 32, 128, device="cuda").to(torch.bfloat16)
+    ws, flush = workspace(H8B), torch.zeros(64 << 20, device="cuda")
+    want = None
+    for turn in range(24):
+        if turn % 2 == 0:
+            flush.add_(1.0)
+        out, lse = torch.zeros_like(q), torch.zeros(P.rows, 32, device="cuda")
+        tg.tern_paged_attn(q, 0.09, cache, batch, out, ws, max_rows, lse)
+        if want is None:
+            want = (out, lse)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), turn
+    check_attention(P, q.double().cpu().numpy(), 0.09, host(out), host(lse))
+
+
 def test_bad_device_data_is_reported_and_left_out():
     """Lengths, row ranges and pages that only the device can see: flagged, nothing outside is touched."""
     heads = (4, 2, 128)
