@@ -6,8 +6,8 @@
 // rows that fall into one 16-token block of one sequence (without a cache: the window itself).
 // The unit's rotation angles are the same for every head, so the CTA computes their sines and
 // cosines once into shared memory, and its warps then take heads in turn: a query head streams
-// its rows through; a key or value head holds its up to 16 rows in registers, because the block's
-// scale (an absmax over all of them) must be known before the first code. A lane holds the same
+// its rows through once, a key or value head twice, because the block's scale (an absmax over all of
+// them) must be known before the first code. A lane holds the same
 // D/64 elements of both halves of a head, so the rotation needs no exchange between lanes.
 // One warp owns one (block, head): no atomics, and the result does not depend on the schedule.
 #include <cstdint>
@@ -133,34 +133,33 @@ __device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 64>& h
   else *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
 }
 
-// A key or value head of one unit: cnt rows from `row`, at places first .. first + cnt - 1 of the block.
+// A key or value head of one unit: cnt rows from `row`, at places first .. first + cnt - 1 of the block. The rows are read
+// twice, for the absmax and for the codes (the second time from the caches): holding 16 rows of a head would take 64
+// registers a lane and leave half the warps.
 template <int D, bool BF16>
 __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int hk, int row, int cnt, int first, int page,
                                             int place, const float2 (*tab)[D / 2], int lane) {
   constexpr int V = D / 64;
   const KvView& kv = p.kv;
-  const int head = p.q_heads + (is_k ? 0 : kv.kv_heads) + hk;
-  Halves<V> x[TERN_KV_BLOCK];
-#pragma unroll
-  for (int j = 0; j < TERN_KV_BLOCK; ++j)
-    if (j < cnt) x[j] = load_head<D, BF16>(p.src, (int64_t)(row + j) * p.stride + (int64_t)head * D, lane);
+  const int64_t src = (int64_t)row * p.stride + (int64_t)(p.q_heads + (is_k ? 0 : kv.kv_heads) + hk) * D;
   const int64_t blk = ((int64_t)page * kv.kv_heads + hk) * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK;
   float* scale = (is_k ? kv.ks : kv.vs) + blk;
   int8_t* codes = (is_k ? kv.k : kv.v) + blk * (TERN_KV_BLOCK * D);
   const float old = first ? *scale : 0.0f;
-  if (is_k) {
-    const Halves<V> g = load_gain<D>(p.k_gain, lane);
-#pragma unroll
-    for (int j = 0; j < TERN_KV_BLOCK; ++j)
-      if (j < cnt) norm_rope<D>(x[j], g, p.k_gain != nullptr, p.eps, &tab[j][lane * V]);
-  }
+  const bool norm = is_k && p.k_gain;
+  const Halves<V> g = load_gain<D>(norm ? p.k_gain : nullptr, lane);
+  auto value = [&](int j) {
+    Halves<V> x = load_head<D, BF16>(p.src, src + j * p.stride, lane);
+    if (is_k) norm_rope<D>(x, g, norm, p.eps, &tab[j][lane * V]);
+    return x;
+  };
   float top = 0.0f;
+#pragma unroll 4
+  for (int j = 0; j < cnt; ++j) {
+    const Halves<V> x = value(j);
 #pragma unroll
-  for (int j = 0; j < TERN_KV_BLOCK; ++j)
-    if (j < cnt) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) top = fmaxf(top, fmaxf(fabsf(x[j].lo[e]), fabsf(x[j].hi[e])));
-    }
+    for (int e = 0; e < V; ++e) top = fmaxf(top, fmaxf(fabsf(x.lo[e]), fabsf(x.hi[e])));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const float s = fmaxf(fmaxf(old, __fdiv_rn(top, 127.0f)), kKvScaleFloor);
@@ -174,14 +173,13 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
       for (int e = 0; e < D / 32; ++e) c[e] = (int8_t)__float2int_rn((float)c[e] * f);
     }
   }
-#pragma unroll
-  for (int j = 0; j < TERN_KV_BLOCK; ++j)
-    if (j < cnt) store_codes<D>(codes + (first + j) * D, x[j], inv, lane);
+#pragma unroll 4
+  for (int j = 0; j < cnt; ++j) store_codes<D>(codes + (first + j) * D, value(j), inv, lane);
   if (lane == 0 && s != old) *scale = s;
 }
 
 template <int D, bool BF16, bool APPEND, int W>
-__global__ void __launch_bounds__(kQkvThreads, APPEND ? 2 : 4) k_qkv(const __grid_constant__ QkvParams p) {
+__global__ void __launch_bounds__(kQkvThreads, 4) k_qkv(const __grid_constant__ QkvParams p) {
   constexpr int V = D / 64;
   __shared__ float2 tab[kWindow][D / 2];
   __shared__ int seq[W];
