@@ -48,6 +48,7 @@ constexpr uint32_t kMaxPolls = 1u << 26;          // seconds, then a wait for a 
 // What a tile costs beside its chunks (queries in, warps joined, result out), in chunks: measured 2.5 us of a
 // CTA that streams a chunk in 0.7 us.
 constexpr int kTileCost = 4;
+
 template <int D, int R>
 struct Shape {
   // CTAs on an SM: while one joins its warps at the end of a tile, the other's stream goes on. 12 warps on the SM, three to
@@ -77,7 +78,6 @@ struct Shape {
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
 };
 
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -90,6 +90,7 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+
 template <int D, int R>
 __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_attn_stream(const __grid_constant__ AttnMaps a) {
   using SH = Shape<D, R>;
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   long long total, per;
   make_plan<R, kChunk, kTileCost, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
   const long long s0 = per * blockIdx.x;
-  if (s0 >= total) return;
+  if (s0 >= total || too_long(p, per)) return;
   Segments<R, kChunk, kTileCost> sg;                                                    // the CTA's segment at hand
   sg.w.s = plan.s;
   sg.w.b = plan.b;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   sg.w.set(p.group);
   sg.at = plan.at;
   sg.pos = 0;
-  sg.count = (int)min(min(per, total - s0), (long long)INT32_MAX);
+  sg.count = (int)min(per, total - s0);
   bool ok = true;
 
   if (warp >= CW) {
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       Group g{-2, 0.0f, 0.0f};
       const int t = (chunk0 + lane / kBlocks * kProducers) * kChunk + lane % kBlocks * TERN_KV_BLOCK;
       if (t < x.vis) {
-        const int page = __ldg(p.kv.table + (int64_t)x.b * p.kv.max_pages + t / p.page), place = t % p.page;
+        const int page = p.kv.table[(int64_t)x.b * p.kv.max_pages + t / p.page], place = t % p.page;
         g.row = -1;
         if (page >= 0 && page < p.kv.pages) {
           const int head = page * p.kv.kv_heads + x.hk;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       const uint16_t* src = p.q + ((int64_t)(w.s.start + (live ? r / p.group : 0)) * p.q_heads + w.hk * (int)p.group.d + (live ? r % p.group : 0)) * D + t * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        v[i] = live ? ld_nc(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        v[i] = live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     }
     named_sync(1, CW * 32);
     // the CTAs that share the tile's chunks, the first and the last of which lie x0 and x1 after the range's start
-    const int x0 = sg.tile + kTileCost, x1 = x0 + w.chunks - 1, per32 = (int)min(per, (long long)INT32_MAX);
+    const int x0 = sg.tile + kTileCost, x1 = x0 + w.chunks - 1, per32 = (int)per;
     const int c0 = blockIdx.x - (x0 < 0 ? (per32 - 1 - x0) / per32 : 0), c1 = blockIdx.x + (x1 < per32 ? 0 : x1 / per32);
     const bool whole = c0 == c1;
     float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes);

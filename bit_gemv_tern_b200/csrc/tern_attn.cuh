@@ -190,6 +190,13 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, Plan* plan, longl
   __syncthreads();
 }
 
+// A call whose ranges do not fit the kernels' 32-bit chunk counters (hours of work) is left out and reported.
+__device__ __forceinline__ bool too_long(const AttnParams& p, long long per) {
+  if (per < (1ll << 30)) return false;
+  if (p.kv.flag && threadIdx.x == 0) *p.kv.flag = 1;
+  return true;
+}
+
 // The kernel for tiles of many rows (tern_attn_tile.cu).
 size_t attn_tile_workspace_bytes(int head_dim);
 cudaError_t launch_attn_tile(AttnMaps& a, int head_dim, bool pdl, cudaStream_t st);

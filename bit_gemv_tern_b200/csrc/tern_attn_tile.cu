@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
   long long total, per;
   make_plan<kRows, kChunk, kTileCost, kThreads>(p, &plan, warp_sums, total, per);   // ends with a barrier
   const long long s0 = per * blockIdx.x;
-  if (s0 >= total) return;
+  if (s0 >= total || too_long(p, per)) return;
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
             const int t = (off + c) * kChunk + lane * TERN_KV_BLOCK;
             row = -2;
             if (t < vis) {
-              const int page = __ldg(table + t / p.page), place = t % p.page;
+              const int page = table[t / p.page], place = t % p.page;
               row = -1;
               if (page >= 0 && page < p.kv.pages) {
                 const int head = page * p.kv.kv_heads + hk;
@@ -482,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       sg.w.set(p.group);
       sg.at = plan.at;
       sg.pos = 0;
-      sg.count = (int)min(min(per, total - s0), (long long)INT32_MAX);
-      const int per32 = (int)min(per, (long long)INT32_MAX);
+      sg.count = (int)min(per, total - s0);
+      const int per32 = (int)per;
       bool more = sg.next(p, true);
       for (int turn = 0;; ++turn) {
         const int s = turn % kSegments;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
       {
         uint4 v[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = r < valid ? ld_nc(p.q + at * D + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < D / 8; ++i) v[i] = r < valid ? *reinterpret_cast<const uint4*>(p.q + at * D + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
         __nv_bfloat162 top2 = __float2bfloat162_rn(0.0f);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)

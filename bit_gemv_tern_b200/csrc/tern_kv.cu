@@ -38,24 +38,24 @@ __device__ __forceinline__ Halves<D / 64> load_head(const void* src, int64_t at,
   if constexpr (BF16) {
     const uint16_t* s = static_cast<const uint16_t*>(src) + at + lane * V;
     if constexpr (V == 2) {
-      const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(s)), b = __ldg(reinterpret_cast<const uint32_t*>(s + D / 2));
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(s), b = *reinterpret_cast<const uint32_t*>(s + D / 2);
       h.lo[0] = bf16_bits_to_float(a & 0xFFFFu);
       h.lo[1] = __uint_as_float(a & 0xFFFF0000u);
       h.hi[0] = bf16_bits_to_float(b & 0xFFFFu);
       h.hi[1] = __uint_as_float(b & 0xFFFF0000u);
     } else {
-      h.lo[0] = bf16_bits_to_float(__ldg(s));
-      h.hi[0] = bf16_bits_to_float(__ldg(s + D / 2));
+      h.lo[0] = bf16_bits_to_float(s[0]);
+      h.hi[0] = bf16_bits_to_float(s[D / 2]);
     }
   } else {
     const float* s = static_cast<const float*>(src) + at + lane * V;
     if constexpr (V == 2) {
-      const float2 a = __ldg(reinterpret_cast<const float2*>(s)), b = __ldg(reinterpret_cast<const float2*>(s + D / 2));
+      const float2 a = *reinterpret_cast<const float2*>(s), b = *reinterpret_cast<const float2*>(s + D / 2);
       h.lo[0] = a.x; h.lo[1] = a.y;
       h.hi[0] = b.x; h.hi[1] = b.y;
     } else {
-      h.lo[0] = __ldg(s);
-      h.hi[0] = __ldg(s + D / 2);
+      h.lo[0] = s[0];
+      h.hi[0] = s[D / 2];
     }
   }
   return h;
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kQkvThreads, 4) k_qkv(const __grid_constant__ 
     if constexpr (APPEND) {
       b = seq[i];
       if (b < 0) continue;
-      const int start = __ldg(p.kv.row_start + b), end = __ldg(p.kv.row_start + b + 1);
-      pos0 = __ldg(p.kv.kv_len + b) - (end - row);
+      const int start = p.kv.row_start[b], end = p.kv.row_start[b + 1];
+      pos0 = p.kv.kv_len[b] - (end - row);
       if (row != start && pos0 % TERN_KV_BLOCK) continue;       // inside a unit that began earlier
       cnt = min(TERN_KV_BLOCK - pos0 % TERN_KV_BLOCK, end - row);
       __syncthreads();                                          // the last unit's table is done with
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kQkvThreads, 4) k_qkv(const __grid_constant__ 
     // angles in turns, reduced in fp64; the sine and cosine of the remainder in fp32
     for (int t = threadIdx.x; t < cnt * (D / 2); t += kQkvThreads) {
       const int j = t / (D / 2), e = t % (D / 2);
-      const double pos = APPEND ? (double)(pos0 + j) : (double)__ldg(p.pos + row + j);
+      const double pos = APPEND ? (double)(pos0 + j) : (double)p.pos[row + j];
       double turn = pos * (__ldg(p.freq + e) * 0.15915494309189533577);
       turn -= rint(turn);
       float s, c;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kQkvThreads, 4) k_qkv(const __grid_constant__ 
     __syncthreads();
     int page = 0, place = 0;
     if constexpr (APPEND) {
-      page = __ldg(p.kv.table + (int64_t)b * p.kv.max_pages + pos0 / p.kv.page_size);
+      page = p.kv.table[(int64_t)b * p.kv.max_pages + pos0 / p.kv.page_size];
       place = pos0 % p.kv.page_size;
       if (page < 0 || page >= p.kv.pages) {
         if (threadIdx.x == 0 && p.kv.flag) *p.kv.flag = 1;
@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadP
     const int b = seq[threadIdx.x], row = w0 + threadIdx.x;
     int page = -1, place = 0;
     if (b >= 0) {
-      const int pos = __ldg(kv.kv_len + b) - (__ldg(kv.row_start + b + 1) - row);
-      page = __ldg(kv.table + (int64_t)b * kv.max_pages + pos / kv.page_size);
+      const int pos = kv.kv_len[b] - (kv.row_start[b + 1] - row);
+      page = kv.table[(int64_t)b * kv.max_pages + pos / kv.page_size];
       place = pos % kv.page_size;
       if (page < 0 || page >= kv.pages) {
         page = -1;
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadP
     const int page = at[i][0], place = at[i][1];
     if (page < 0) continue;
     const int64_t head = (int64_t)page * kv.kv_heads + hk;
-    const float s = __ldg((is_v ? kv.vs : kv.ks) + head * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK);
-    const uint4 w = ld_nc((is_v ? kv.v : kv.k) + (head * kv.page_size + place) * D + c * 16);
+    const float s = (is_v ? kv.vs : kv.ks)[head * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK];
+    const uint4 w = *reinterpret_cast<const uint4*>((is_v ? kv.v : kv.k) + (head * kv.page_size + place) * D + c * 16);
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
     uint32_t o[8];
 #pragma unroll
@@ -309,20 +309,23 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadP
 
 template <int D, bool BF16, bool APPEND>
 cudaError_t launch_qkv_t(const QkvParams& p, bool pdl, cudaStream_t st) {
-  // windows of one row while the sequences bring fewer than 16 rows each (decode, verify), so that
-  // every block is a CTA's own; windows of 16 rows for longer runs, whose blocks fill up
+  // Appending: windows of one row while the sequences bring fewer than 16 rows each (decode, verify), so that every block is a
+  // CTA's own; windows of 16 rows for longer runs, whose blocks fill up. Without a cache nothing ties rows together:
+  // windows of 8 once there are enough of them (4095 rows: 29.1 us, against 32.6 with 16), one row below.
+  constexpr int kWide = APPEND ? kWindow : kWindow / 2;
   const bool wide = APPEND ? p.rows / p.kv.batch >= kWindow : p.rows >= 64 * kWindow;
-  const int windows = wide ? (p.rows + kWindow - 1) / kWindow : p.rows;
+  const int windows = wide ? (p.rows + kWide - 1) / kWide : p.rows;
   const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
   const int warps = kQkvThreads / 32;
-  // split the heads over CTAs until every SM has eight: a warp then takes one head or a few
-  int split = (8 * device_sm_count() + windows - 1) / windows;
+  // The heads are split over CTAs until every SM has eight (of rows of 8: sixteen): one head a warp hides the look-ups and the
+  // angles best (append of 3.7 k tokens: 43 us, against 58 with four a SM and 77 with two).
+  int split = ((APPEND ? 8 : 16) * device_sm_count() + windows - 1) / windows;
   if (split > (tasks + warps - 1) / warps) split = (tasks + warps - 1) / warps;
   // the fewest CTAs with as many rounds of heads
   const int rounds = (tasks + split * warps - 1) / (split * warps);
   split = (tasks + rounds * warps - 1) / (rounds * warps);
   const dim3 grid(windows, split);
-  return wide ? launch_maybe_pdl(k_qkv<D, BF16, APPEND, kWindow>, grid, dim3(kQkvThreads), 0, pdl, st, p)
+  return wide ? launch_maybe_pdl(k_qkv<D, BF16, APPEND, kWide>, grid, dim3(kQkvThreads), 0, pdl, st, p)
               : launch_maybe_pdl(k_qkv<D, BF16, APPEND, 1>, grid, dim3(kQkvThreads), 0, pdl, st, p);
 }
 

@@ -13,6 +13,9 @@ namespace tern {
 // needs no case of its own (1/s is finite and the codes are 0).
 constexpr float kKvScaleFloor = 8.673617379884035e-19f;      // 2^-60
 
+// What a call reads may have been written by the kernel just before it, beside which programmatic dependent launch
+// starts it: nothing of it goes through the non-coherent path (ld.global.nc).
+
 // Sequence b's rows and tokens, and whether the call can use them.
 struct SeqInfo {
   int start, n, len;
@@ -20,9 +23,9 @@ struct SeqInfo {
 };
 __device__ __forceinline__ SeqInfo seq_info(const KvView& kv, int b) {
   SeqInfo s;
-  const int e = __ldg(kv.row_start + b + 1);
-  s.start = __ldg(kv.row_start + b);
-  s.len = __ldg(kv.kv_len + b);
+  const int e = kv.row_start[b + 1];
+  s.start = kv.row_start[b];
+  s.len = kv.kv_len[b];
   s.ok = s.start >= 0 && e >= s.start && e <= kv.rows && s.len >= 0 && s.len <= kv.max_pages * kv.page_size;
   s.n = s.ok ? e - s.start : 0;
   return s;

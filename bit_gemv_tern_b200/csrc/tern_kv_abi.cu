@@ -39,7 +39,7 @@ tern_status check_kv(const tern_kv_cache* c, const tern_kv_batch* b, int32_t* er
   if (c->pages < 1 || c->page_size < TERN_KV_BLOCK || c->page_size > 65536 || c->page_size % TERN_KV_BLOCK) return TERN_ESHAPE;
   if (!valid_heads(c->kv_heads, c->kv_heads, c->head_dim)) return TERN_ESHAPE;
   if (b->batch < 1 || b->batch > 65536 || b->rows < 0 || b->rows > kMaxRows || b->max_pages < 1 ||
-      (int64_t)b->max_pages * c->page_size > INT32_MAX || (int64_t)c->pages * c->kv_heads * c->page_size > INT32_MAX)
+      (int64_t)b->max_pages * c->page_size > INT32_MAX - 65536 || (int64_t)c->pages * c->kv_heads * c->page_size > INT32_MAX)
     return TERN_ESHAPE;
   if (!aligned(c->k_dev, 16) || !aligned(c->v_dev, 16) || !aligned(c->k_scale_dev, 4) || !aligned(c->v_scale_dev, 4) ||
       !aligned(b->row_start_dev, 4) || !aligned(b->kv_len_dev, 4) || !aligned(b->page_table_dev, 4) || !aligned(err_flag_dev, 4))

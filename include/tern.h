@@ -544,12 +544,12 @@ tern_status fv5b_head_gemv_argmax(const int8_t* W_dev, const float* block_scale_
  *
  * row_start, kv_len and page_table live on the device and may change between the replays of a
  * captured call. What only the device can see of them is checked there: a sequence with row_start
- * decreasing or outside 0 .. rows, or with kv_len negative or past max_pages * page_size, is left
- * out (its outputs stay as they were), a page outside 0 .. pages - 1 is neither read nor written
- * (its tokens are not seen, its rows are not returned), and *err_flag_dev, if given, is set
- * nonzero. The flag is never cleared by these calls (clear it once; tern_read_flag reads it).
- * Pages that two sequences share may be read by both; no two sequences of a call may append into
- * one page. */
+ * decreasing or outside 0 .. rows, with kv_len negative or past max_pages * page_size, or (to append
+ * or read back) with kv_len below n_b, is left out (its outputs stay as they were); a page outside
+ * 0 .. pages - 1 is neither read nor written (its tokens are not seen, its rows are not returned); and
+ * *err_flag_dev, if given, is set nonzero. The flag is never cleared by these calls (clear it once;
+ * tern_read_flag reads it). Pages that two sequences share may be read by both; no two sequences of a
+ * call may append into one page. */
 typedef enum { TERN_ELEM_F32 = 0, TERN_ELEM_BF16 = 1 } tern_elem;
 
 /* Tokens that share one scale. */
@@ -569,7 +569,7 @@ typedef struct {
 typedef struct {
   int32_t batch;                  /* sequences, 1 .. 65536                                      */
   int32_t rows;                   /* activation rows, 0 .. 2^24 (0: nothing is enqueued)        */
-  int32_t max_pages;              /* entries per page_table row; max_pages * page_size < 2^31   */
+  int32_t max_pages;              /* entries per page_table row; max_pages * page_size < 2^31 - 2^16 */
   const int32_t* row_start_dev;   /* [batch + 1]                                                */
   const int32_t* kv_len_dev;      /* [batch]                                                    */
   const int32_t* page_table_dev;  /* [batch][max_pages]                                         */
@@ -634,7 +634,8 @@ size_t tern_paged_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_
  *   gives the right result.
  *   workspace_dev: at least tern_paged_attn_workspace_bytes bytes, 16-byte aligned, zero-filled
  *   before its first use; every call leaves its counters zero again, so one buffer serves any number of
- *   calls in stream order (two calls, or two captured graphs, that overlap in time need two).
+ *   calls in stream order (two calls, or two captured graphs, that overlap in time need two). After
+ *   TERN_ETIMEOUT (tern_device_status) it has to be zero-filled again.
  * Codes and queries are multiplied exactly (the queries as fp16 scaled by a power of two of
  * their row's absmax), sums, maxima and the softmax are fp32, the probabilities times the value
  * block's scale are rounded to fp16 for the second product. |value| below 2^27 keeps that scaling
