@@ -15,7 +15,7 @@
 //           the lengths). A tile that spans CTAs
 //           leaves a partial result (max, sum, unnormalised output) per CTA in the workspace; the last
 //           CTA to arrive, by a counter, joins them in CTA order, so results do not depend on timing.
-//   Warps.  A producer warp or two; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
+//   Warps.  One producer warp; each consumer warp takes whole 16-token blocks in turn and keeps a softmax
 //           of its own (max, sum, output in registers); the warps' results are joined once per tile.
 //   Math.   S^T = K Q^T and O^T = V^T P^T with mma.sync m16n8k16 f16: the 16 tokens of a block are the
 //           M side of the first product, so a block's scale is one number per instruction, and the
@@ -53,11 +53,11 @@ template <int D, int R>
 struct Shape {
   // CTAs on an SM: while one joins its warps at the end of a tile, the other's stream goes on. 12 warps on the SM, three to
   // a register file partition (168 registers a thread), for 32 rows 8 (255 registers); 16 warps with 128 registers were
-  // 2% slower for 8 rows.
+  // 2% slower for 8 rows. One warp of a CTA produces: a second one for 32 rows, a consumer less, was 9% slower (16 sequences of
+  // 8 rows, 77.4 against 71.2 us).
   static constexpr int kPerSM = R == 32 ? 1 : 2;
-  static constexpr int kProducers = R == 32 ? 2 : 1;
-  static constexpr int kCW = (R == 32 ? 8 : 12) / kPerSM - kProducers;   // consumer warps
-  static constexpr int kThreads = (kCW + kProducers) * 32;
+  static constexpr int kCW = (R == 32 ? 8 : 12) / kPerSM - 1;     // consumer warps
+  static constexpr int kThreads = (kCW + 1) * 32;
   static constexpr int kNT = R / 8;                               // 8-row column groups
   static constexpr int kTiles = D / 16;                           // 16-element tiles of a head
   static constexpr int kHalfStage = kChunk * D;                   // bytes of a stage's keys
@@ -94,7 +94,7 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 template <int D, int R>
 __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_attn_stream(const __grid_constant__ AttnMaps a) {
   using SH = Shape<D, R>;
-  constexpr int CW = SH::kCW, kProducers = SH::kProducers, NT = SH::kNT, T = SH::kTiles, ST = SH::kStages;
+  constexpr int CW = SH::kCW, NT = SH::kNT, T = SH::kTiles, ST = SH::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base - raw);
@@ -137,16 +137,16 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   sg.count = (int)min(per, total - s0);
   bool ok = true;
 
-  if (warp >= CW) {
-    // ---------------- producers: pages, scales and boxes, a group of 32 blocks looked up ahead ----------------
+  if (warp == CW) {
+    // ---------------- producer: pages, scales and boxes, a group of 32 blocks looked up ahead ----------------
     struct Group {
       int row;                 // first row of the block in the tensor maps, -1: no such page, -2: past the end
       float ks, vs;
     };
-    // lane: block lane % 4 of the chunk that this warp issues lane / 4 turns after chunk0
+    // lane: block lane % 4 of the chunk lane / 4 after chunk0
     auto look = [&](const auto& x, int chunk0) -> Group {
       Group g{-2, 0.0f, 0.0f};
-      const int t = (chunk0 + lane / kBlocks * kProducers) * kChunk + lane % kBlocks * TERN_KV_BLOCK;
+      const int t = (chunk0 + lane / kBlocks) * kChunk + lane % kBlocks * TERN_KV_BLOCK;
       if (t < x.vis) {
         const int page = p.kv.table[(int64_t)x.b * p.kv.max_pages + t / p.page], place = t % p.page;
         g.row = -1;
@@ -162,29 +162,27 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       }
       return g;
     };
-    constexpr int kAhead = 32 / kBlocks;         // turns of a group
+    constexpr int kAhead = 32 / kBlocks;         // chunks of a group
     // blocks of a chunk that begin a box
     const uint32_t boxes = p.box == 64 ? 1u : p.box == 32 ? 5u : 15u;
-    const int me = warp - CW;
-    int q0 = 0, last = -1;                       // ring position of the segment; of this warp's last stage
+    int q0 = 0, last = -1;                       // ring position of the segment; of the last stage
     Group cur, nxt;
     bool ready = false;                          // nxt is the segment's first group
     for (bool more = sg.next(p, true); more && ok; more = sg.next(p, false)) {
       const int seg = sg.seg;
-      const int c0 = (me + kProducers - q0 % kProducers) % kProducers;
-      if (!ready) nxt = look(sg.w, sg.off + c0);
+      if (!ready) nxt = look(sg.w, sg.off);
       ready = false;
       int at = 0;
-      for (int c = c0; c < seg; c += kProducers) {
+      for (int c = 0; c < seg; ++c) {
         const int q = q0 + c, s = q % ST;
         if (at == 0) {                           // look the next group up while this one is copied
           cur = nxt;
-          if (c + kAhead * kProducers < seg) {
-            nxt = look(sg.w, sg.off + c + kAhead * kProducers);
+          if (c + kAhead < seg) {
+            nxt = look(sg.w, sg.off + c + kAhead);
           } else {
             Segments<R, kChunk, kTileCost> x = sg;
             ready = x.next(p, false);
-            if (ready) nxt = look(x.w, x.off + (me + kProducers - (q0 + seg) % kProducers) % kProducers);
+            if (ready) nxt = look(x.w, x.off);
           }
         }
         if (q >= ST && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * s, ((q / ST) - 1) & 1)))) break;
@@ -218,7 +216,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       q0 += seg;
     }
     // do not leave with copies in flight (bounded, also after a give-up)
-    for (int r = last; r >= 0 && r > last - ST; r -= kProducers)
+    for (int r = last; r >= 0 && r > last - ST; --r)
       if (!mbar_wait(full + 8 * (r % ST), (r / ST) & 1)) { ok = false; break; }
     if (!ok && lane == 0) atomicExch(&g_attn_latch, 5);
     return;
