@@ -68,7 +68,9 @@ struct Shape {
   static __device__ __forceinline__ int place(int d) { return D == 128 ? d + 4 * (((d >> 4) + 1) >> 1) : d + 4 * (d >> 4); }
   // stages | join buffer [warp][R][pitch] | max, sum [warp][R] each | scales [stage][block][4] | masks, stage numbers | barriers
   static constexpr int kOffJoin = kStages * 2 * kHalfStage;
-  static constexpr int kOffMax = kOffJoin + kCW * R * kRowPitch * 4;
+  // the join buffer also takes the max and sum of a tile's partial results, one of every CTA at most
+  static constexpr int kJoinFloats = kCW * R * kRowPitch, kPartMaxima = 2 * kPerSM * kMaxGridCTAs * R;
+  static constexpr int kOffMax = kOffJoin + (kJoinFloats > kPartMaxima ? kJoinFloats : kPartMaxima) * 4;
   static constexpr int kOffSum = kOffMax + kCW * R * 4;
   static constexpr int kOffScale = kOffSum + kCW * R * 4;
   static constexpr int kOffMask = kOffScale + kStages * 4 * kBlocks * 4;
@@ -558,6 +560,7 @@ cudaError_t launch_stream_t(AttnMaps& a, bool pdl, cudaStream_t st) {
   static std::atomic<unsigned long long> smem_raised{0};
   cudaError_t e = allow_max_dynamic_smem(k_attn_stream<D, R>, smem_raised);
   if (e != cudaSuccess) return e;
+  static_assert((Shape<D, R>::kSmem + 1024) * Shape<D, R>::kPerSM <= 228 * 1024, "the CTAs of an SM share its memory");
   a.p.grid = fast_div(persistent_grid(kMaxGridCTAs) * Shape<D, R>::kPerSM);
   return launch_maybe_pdl(k_attn_stream<D, R>, dim3(a.p.grid.d), dim3(Shape<D, R>::kThreads),
                           Shape<D, R>::kSmem, pdl, st, a);

@@ -305,6 +305,12 @@ def test_attention_over_a_long_cache_and_again():
     run_attn(Paged(73, heads, 16, [(1, 3000)]), 74, ws=ws)
 
 
+@pytest.mark.parametrize("heads,n", [((4, 1, 64), 1), ((4, 1, 64), 4), ((8, 1, 64), 4), ((8, 1, 128), 1), ((8, 1, 128), 4), ((8, 1, 64), 9)])
+def test_attention_of_one_tile_over_every_cta(heads, n):
+    """One key/value head and one sequence of 292 chunks of 64 tokens: as many CTAs leave a partial result of the one tile."""
+    run_attn(Paged(76, heads, 64, [(n, 18_688)]), 77)
+
+
 @pytest.mark.parametrize("lens,max_rows", [([(1, 30_000), (1, 900)], 1), ([(4, 12_000)], 4), ([(8, 12_000)], 8), ([(200, 6000)], 200)])
 def test_attention_gives_the_same_bits_whether_its_cache_is_cold_or_not(lens, max_rows):
     """Stages that arrive late and out of order (pages scattered over memory, the L2 flushed) change nothing."""
