@@ -46,8 +46,10 @@ constexpr int kChunk = 64;                        // tokens of a stage: four blo
 constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
 constexpr uint32_t kMaxPolls = 1u << 26;          // seconds, then a wait for a stage gives up
 // What a tile costs beside its chunks (queries in, warps joined, result out), in chunks: measured 2.5 us of a
-// CTA that streams a chunk in 0.7 us.
-constexpr int kTileCost = 4;
+// CTA that streams a chunk in 0.7 us; with 32 rows and one CTA on the SM 6 to 8 us, of which the last CTA of a tile spends 4
+// on joining the partial results (16 ragged sequences of 8 rows: 71.4 us with a cost of 4, 65.4 with 8, 65.7 with 10).
+template <int R>
+constexpr int kTileCost = R == 32 ? 8 : 4;
 
 template <int D, int R>
 struct Shape {
@@ -74,8 +76,8 @@ struct Shape {
   static constexpr int kOffSum = kOffMax + kCW * R * 4;
   static constexpr int kOffScale = kOffSum + kCW * R * 4;
   static constexpr int kOffMask = kOffScale + kStages * 4 * kBlocks * 4;
-  static constexpr int kOffQ = kOffMask + kStages * 8;            // R = 32: query fragments [step][NT / 2][32] x 16 B
-  static constexpr int kOffBar = kOffQ + (R == 32 ? D / 16 * kNT * 256 : 0);
+  static constexpr int kOffQ = kOffMask + kStages * 8;            // R = 32: query fragments [step][NT / 2][32] x 16 B, row factors
+  static constexpr int kOffBar = kOffQ + (R == 32 ? D / 16 * kNT * 256 + 4 * R : 0);
   static constexpr int kSmem = kOffBar + kStages * 16 + 1024;
   static constexpr int kPartFloats = R * D + 2 * R;               // a partial result in the workspace
 };
@@ -125,10 +127,10 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
   pdl_wait();
   pdl_launch_dependents();
   long long total, per;
-  make_plan<R, kChunk, kTileCost, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
+  make_plan<R, kChunk, kTileCost<R>, SH::kThreads>(p, &plan, warp_sums, total, per);       // ends with a barrier
   const long long s0 = per * blockIdx.x;
   if (s0 >= total || too_long(p, per)) return;
-  Segments<R, kChunk, kTileCost> sg;                                                    // the CTA's segment at hand
+  Segments<R, kChunk, kTileCost<R>> sg;                                                    // the CTA's segment at hand
   sg.w.s = plan.s;
   sg.w.b = plan.b;
   sg.w.hk = plan.hk;
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
           if (c + kAhead < seg) {
             nxt = look(sg.w, sg.off + c + kAhead);
           } else {
-            Segments<R, kChunk, kTileCost> x = sg;
+            Segments<R, kChunk, kTileCost<R>> x = sg;
             ready = x.next(p, false);
             if (ready) nxt = look(x.w, x.off);
           }
@@ -236,8 +238,11 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     // queries as fp16 fragments, each row scaled by a power of two into [2^13, 2^14)
     uint32_t qf[R == 32 ? 1 : NT][R == 32 ? 1 : T][2];
     float rowf[NT][2], m[NT][2], l[NT][2], o[T][NT][4];
+    // for 32 rows, 8 by each of four warps, which leave them in shared memory (every warp for itself: 65.4 against 62.5 us)
+    static_assert(R < 32 || CW >= NT);
+    float* srow = reinterpret_cast<float*>(sm + SH::kOffQ + D / 16 * NT * 256);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = R == 32 ? warp : 0; n < NT; n += R == 32 ? NT : 1) {
       const int r = row0 + 8 * n + g;
       uint4 v[D / 32];
       float top = 0.0f;
@@ -256,8 +261,12 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
       const int E = absmax_exponent(top);
       const float up = exp2f_i(14 - E);
       const float f = p.scale * kLog2e * exp2f_i(E - 14);
-      rowf[n][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);               // rows 2t, 2t + 1 of the group of eight
-      rowf[n][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+      if constexpr (R == 32) {
+        if (t == 0) srow[8 * n + g] = f;
+      } else {
+        rowf[n][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);             // rows 2t, 2t + 1 of the group of eight
+        rowf[n][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+      }
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -265,20 +274,29 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
         for (int e = 0; e < 4; ++e) {
           const uint32_t h = pack_f16(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xFFFF0000u) * up);
           if constexpr (R == 32) {
-            // step 2i + e/2 of the fragments in shared memory; every warp writes the same
-            uint32_t* sq = reinterpret_cast<uint32_t*>(sm + SH::kOffQ);
-            if (warp == n) sq[(((2 * i + (e >> 1)) * (NT / 2) + n / 2) * 32 + lane) * 4 + (n & 1) * 2 + (e & 1)] = h;
+            uint32_t* sq = reinterpret_cast<uint32_t*>(sm + SH::kOffQ);      // step 2i + e/2 of the fragments
+            sq[(((2 * i + (e >> 1)) * (NT / 2) + n / 2) * 32 + lane) * 4 + (n & 1) * 2 + (e & 1)] = h;
           } else {
             qf[n][2 * i + (e >> 1)][e & 1] = h;
           }
         }
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = kNoMax;
       l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < T; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
     }
-    if constexpr (R == 32) named_sync(1, CW * 32);
+    if constexpr (R == 32) {
+      named_sync(1, CW * 32);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        rowf[n][0] = srow[8 * n + 2 * t];
+        rowf[n][1] = srow[8 * n + 2 * t + 1];
+      }
+    }
     // tokens below this are seen by every row of the tile
     const int clear = max(0, w.s.len - w.s.n + row0 / p.group + 1);
     const int phase = q0 * kBlocks % CW;                             // the warp that takes the first block
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
     }
     named_sync(1, CW * 32);
     // the CTAs that share the tile's chunks, the first and the last of which lie x0 and x1 after the range's start
-    const int x0 = sg.tile + kTileCost, x1 = x0 + w.chunks - 1, per32 = (int)per;
+    const int x0 = sg.tile + kTileCost<R>, x1 = x0 + w.chunks - 1, per32 = (int)per;
     const int c0 = blockIdx.x - (x0 < 0 ? (per32 - 1 - x0) / per32 : 0), c1 = blockIdx.x + (x1 < per32 ? 0 : x1 / per32);
     const bool whole = c0 == c1;
     float* parts = reinterpret_cast<float*>(p.ws + kCounterBytes);
