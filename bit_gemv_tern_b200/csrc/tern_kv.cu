@@ -7,8 +7,8 @@
 // The unit's rotation angles are the same for every head, so the CTA computes their sines and
 // cosines once into shared memory, and its warps then take heads in turn: a query head streams
 // its rows through once, a key or value head twice, because the block's scale (an absmax over all of
-// them) must be known before the first code. A lane holds the same
-// D/64 elements of both halves of a head, so the rotation needs no exchange between lanes.
+// them) must be known before the first code. A half-warp takes a row; a lane holds the same
+// D/32 elements of both halves of a head, so the rotation needs no exchange between lanes.
 // One warp owns one (block, head): no atomics, and the result does not depend on the schedule.
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -25,88 +25,102 @@ constexpr int kQkvThreads = 256;
 constexpr int kWindow = 16;                     // rows of a window (decode batches take windows of one row)
 constexpr int kReadWindow = 16;
 
-// One head's elements of a lane: lane * V .. of the first half and of the second half.
+// One head's elements of a lane: of its row's 16 lanes lane l holds l * V .. of the first half and of the second half.
 template <int V>
 struct Halves {
   float lo[V], hi[V];
 };
 
-template <int D, bool BF16>
-__device__ __forceinline__ Halves<D / 64> load_head(const void* src, int64_t at, int lane) {
-  constexpr int V = D / 64;
-  Halves<V> h;
+template <int V, bool BF16>
+__device__ __forceinline__ void load_some(float (&x)[V], const void* src, int64_t at) {
   if constexpr (BF16) {
-    const uint16_t* s = static_cast<const uint16_t*>(src) + at + lane * V;
-    if constexpr (V == 2) {
-      const uint32_t a = *reinterpret_cast<const uint32_t*>(s), b = *reinterpret_cast<const uint32_t*>(s + D / 2);
-      h.lo[0] = bf16_bits_to_float(a & 0xFFFFu);
-      h.lo[1] = __uint_as_float(a & 0xFFFF0000u);
-      h.hi[0] = bf16_bits_to_float(b & 0xFFFFu);
-      h.hi[1] = __uint_as_float(b & 0xFFFF0000u);
+    uint32_t w[V / 2];
+    if constexpr (V == 4) {
+      const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(src) + at);
+      w[0] = y.x; w[1] = y.y;
     } else {
-      h.lo[0] = bf16_bits_to_float(s[0]);
-      h.hi[0] = bf16_bits_to_float(s[D / 2]);
+      w[0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(src) + at);
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  } else if constexpr (V == 4) {
+    const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+    x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
   } else {
-    const float* s = static_cast<const float*>(src) + at + lane * V;
-    if constexpr (V == 2) {
-      const float2 a = *reinterpret_cast<const float2*>(s), b = *reinterpret_cast<const float2*>(s + D / 2);
-      h.lo[0] = a.x; h.lo[1] = a.y;
-      h.hi[0] = b.x; h.hi[1] = b.y;
-    } else {
-      h.lo[0] = s[0];
-      h.hi[0] = s[D / 2];
-    }
+    const float2 y = *reinterpret_cast<const float2*>(static_cast<const float*>(src) + at);
+    x[0] = y.x; x[1] = y.y;
   }
+}
+
+template <int D, bool BF16>
+__device__ __forceinline__ Halves<D / 32> load_head(const void* src, int64_t at, int l) {
+  constexpr int V = D / 32;
+  Halves<V> h;
+  load_some<V, BF16>(h.lo, src, at + l * V);
+  load_some<V, BF16>(h.hi, src, at + D / 2 + l * V);
   return h;
 }
 
-template <int V>
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the 16 lanes of a row.
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
 // Norm (where there is a gain), then rotation by this lane's cosines and sines.
 template <int D>
-__device__ __forceinline__ void norm_rope(Halves<D / 64>& h, const Halves<D / 64>& g, bool norm, float eps,
+__device__ __forceinline__ void norm_rope(Halves<D / 32>& h, const Halves<D / 32>& g, bool norm, float eps,
                                           const float2* tab) {
-  constexpr int V = D / 64;
+  constexpr int V = D / 32;
   float r = 1.0f;
   if (norm) {
     float ss = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; ++e) ss += h.lo[e] * h.lo[e] + h.hi[e] * h.hi[e];
-    ss = warp_sum<V>(ss);
+    ss = row_sum(ss);
     r = rsqrtf(ss * (1.0f / D) + eps);
   }
+  float4 two;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
+    if (e % 2 == 0) two = *reinterpret_cast<const float4*>(tab + e);
     const float a = norm ? h.lo[e] * r * g.lo[e] : h.lo[e], b = norm ? h.hi[e] * r * g.hi[e] : h.hi[e];
-    const float2 t = tab[e];
+    const float2 t = e & 1 ? make_float2(two.z, two.w) : make_float2(two.x, two.y);
     h.lo[e] = a * t.x - b * t.y;
     h.hi[e] = b * t.x + a * t.y;
   }
 }
 
-template <int D>
-__device__ __forceinline__ void store_bf16(uint16_t* dst, const Halves<D / 64>& h, int lane) {
-  constexpr int V = D / 64;
-  if constexpr (V == 2) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(h.lo[0], h.lo[1]), b = __floats2bfloat162_rn(h.hi[0], h.hi[1]);
-    *reinterpret_cast<__nv_bfloat162*>(dst + lane * 2) = a;
-    *reinterpret_cast<__nv_bfloat162*>(dst + D / 2 + lane * 2) = b;
-  } else {
-    *reinterpret_cast<__nv_bfloat16*>(dst + lane) = __float2bfloat16_rn(h.lo[0]);
-    *reinterpret_cast<__nv_bfloat16*>(dst + D / 2 + lane) = __float2bfloat16_rn(h.hi[0]);
-  }
+template <int V>
+__device__ __forceinline__ void store_some_bf16(uint16_t* dst, const float (&x)[V]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[V - 2], x[V - 1]);
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&a), w = *reinterpret_cast<const uint32_t*>(&b);
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u, w);
+  else *reinterpret_cast<uint32_t*>(dst) = u;
 }
 
 template <int D>
-__device__ __forceinline__ Halves<D / 64> load_gain(const uint16_t* gain, int lane) {
-  if (gain) return load_head<D, true>(gain, 0, lane);
-  return Halves<D / 64>{};
+__device__ __forceinline__ void store_bf16(uint16_t* dst, const Halves<D / 32>& h, int l) {
+  store_some_bf16<D / 32>(dst + l * (D / 32), h.lo);
+  store_some_bf16<D / 32>(dst + D / 2 + l * (D / 32), h.hi);
+}
+
+// Gains are aligned to 4 bytes only.
+template <int D>
+__device__ __forceinline__ Halves<D / 32> load_gain(const uint16_t* gain, int l) {
+  Halves<D / 32> g{};
+  if (gain) {
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2) {
+      float x[2];
+      load_some<2, true>(x, gain, l * (D / 32) + e);
+      g.lo[e] = x[0]; g.lo[e + 1] = x[1];
+      load_some<2, true>(x, gain, D / 2 + l * (D / 32) + e);
+      g.hi[e] = x[0]; g.hi[e + 1] = x[1];
+    }
+  }
+  return g;
 }
 
 // clamp(rint(x * inv), -127, 127) in the low byte: adding 1.5 * 2^23 rounds to an integer and leaves it in the low bits (the
@@ -115,23 +129,20 @@ __device__ __forceinline__ uint32_t code_of(float x, float inv) {
   return __float_as_uint(fminf(fmaxf(x * inv, -127.0f), 127.0f) + 12582912.0f);
 }
 
-// The codes of one token in one block: a lane's 2V codes leave as one store, after neighbours have
-// traded halves (the even lane writes the first half's, the odd lane the second half's).
-template <int D>
-__device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 64>& h, float inv, int lane) {
-  constexpr int V = D / 64;
-  uint32_t lo = 0, hi = 0;
+template <int V>
+__device__ __forceinline__ void store_some_codes(int8_t* dst, const float (&x)[V], float inv) {
+  uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    lo |= (code_of(h.lo[e], inv) & 0xFFu) << (8 * e);
-    hi |= (code_of(h.hi[e], inv) & 0xFFu) << (8 * e);
-  }
-  const bool odd = lane & 1;
-  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
-  const uint32_t w = odd ? (got | (hi << (8 * V))) : (lo | (got << (8 * V)));
-  int8_t* at = dst + (odd ? D / 2 : 0) + (lane >> 1) * 2 * V;
-  if constexpr (V == 2) *reinterpret_cast<uint32_t*>(at) = w;
-  else *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+  for (int e = 0; e < V; ++e) w |= (code_of(x[e], inv) & 0xFFu) << (8 * e);
+  if constexpr (V == 4) *reinterpret_cast<uint32_t*>(dst) = w;
+  else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
+}
+
+// The codes of one token in one block.
+template <int D>
+__device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 32>& h, float inv, int l) {
+  store_some_codes<D / 32>(dst + l * (D / 32), h.lo, inv);
+  store_some_codes<D / 32>(dst + D / 2 + l * (D / 32), h.hi, inv);
 }
 
 // A key or value head of one unit: cnt rows from `row`, at places first .. first + cnt - 1 of the block. The rows are read
@@ -140,7 +151,8 @@ __device__ __forceinline__ void store_codes(int8_t* dst, const Halves<D / 64>& h
 template <int D, bool BF16>
 __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int hk, int row, int cnt, int first, int page,
                                             int place, const float2 (*tab)[D / 2], int lane) {
-  constexpr int V = D / 64;
+  constexpr int V = D / 32;
+  const int l = lane & 15, sub = lane >> 4;
   const KvView& kv = p.kv;
   const int64_t src = (int64_t)row * p.stride + (int64_t)(p.q_heads + (is_k ? 0 : kv.kv_heads) + hk) * D;
   const int64_t blk = ((int64_t)page * kv.kv_heads + hk) * (kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK;
@@ -148,16 +160,16 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
   int8_t* codes = (is_k ? kv.k : kv.v) + blk * (TERN_KV_BLOCK * D);
   const float old = first ? *scale : 0.0f;
   const bool norm = is_k && p.k_gain;
-  const Halves<V> g = load_gain<D>(norm ? p.k_gain : nullptr, lane);
+  const Halves<V> g = load_gain<D>(norm ? p.k_gain : nullptr, l);
   auto value = [&](int j) {
-    Halves<V> x = load_head<D, BF16>(p.src, src + j * p.stride, lane);
-    if (is_k) norm_rope<D>(x, g, norm, p.eps, &tab[j][lane * V]);
+    Halves<V> x = load_head<D, BF16>(p.src, src + j * p.stride, l);
+    if (is_k) norm_rope<D>(x, g, norm, p.eps, &tab[j][l * V]);
     return x;
   };
   float top = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < cnt; ++j) {
-    const Halves<V> x = value(j);
+#pragma unroll 2
+  for (int j = 0; j < cnt; j += 2) {                            // two rows at a time, the last alone by both half-warps
+    const Halves<V> x = value(min(j + sub, cnt - 1));
 #pragma unroll
     for (int e = 0; e < V; ++e) top = fmaxf(top, fmaxf(fabsf(x.lo[e]), fabsf(x.hi[e])));
   }
@@ -174,15 +186,20 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
       for (int e = 0; e < D / 32; ++e) c[e] = (int8_t)__float2int_rn((float)c[e] * f);
     }
   }
-#pragma unroll 4
-  for (int j = 0; j < cnt; ++j) store_codes<D>(codes + (first + j) * D, value(j), inv, lane);
+#pragma unroll 2
+  for (int j = 0; j < cnt; j += 2) {
+    const Halves<V> x = value(min(j + sub, cnt - 1));
+    if (j + sub < cnt) store_codes<D>(codes + (first + j + sub) * D, x, inv, l);
+  }
   if (lane == 0 && s != old) *scale = s;
 }
 
+// 64 registers a thread where it appends, 51 where not: 36.4 and 23.1 us (append with read-back, 3.7 k tokens; rotation, 4095
+// rows); with one CTA more on the SM 38.2 and 24.7, with one less 38.2 and 23.8.
 template <int D, bool BF16, bool APPEND, int W>
-__global__ void __launch_bounds__(kQkvThreads, APPEND ? 4 : 6) k_qkv(const __grid_constant__ QkvParams p) {
-  constexpr int V = D / 64;
-  __shared__ float2 tab[kWindow][D / 2];
+__global__ void __launch_bounds__(kQkvThreads, APPEND ? 4 : 5) k_qkv(const __grid_constant__ QkvParams p) {
+  constexpr int V = D / 32;
+  __shared__ __align__(16) float2 tab[kWindow][D / 2];
   __shared__ int seq[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w0 = blockIdx.x * W, wn = min(W, p.rows - w0);
@@ -245,14 +262,16 @@ __global__ void __launch_bounds__(kQkvThreads, APPEND ? 4 : 6) k_qkv(const __gri
       const int h = APPEND ? t - 2 * p.kv_heads : t;            // source head: queries, then keys
       const bool is_q = h < p.q_heads;
       const uint16_t* gain = is_q ? p.q_gain : p.k_gain;
-      const Halves<V> g = load_gain<D>(gain, lane);
+      const int l = lane & 15, sub = lane >> 4;
+      const Halves<V> g = load_gain<D>(gain, l);
       uint16_t* dst = is_q ? p.q + ((int64_t)row * p.q_heads + h) * D : p.k + ((int64_t)row * p.kv_heads + h - p.q_heads) * D;
       const int64_t step = (int64_t)(is_q ? p.q_heads : p.kv_heads) * D;
-#pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
-        Halves<V> x = load_head<D, BF16>(p.src, (int64_t)(row + j) * p.stride + (int64_t)h * D, lane);
-        norm_rope<D>(x, g, gain != nullptr, p.eps, &tab[j][lane * V]);
-        store_bf16<D>(dst + j * step, x, lane);
+#pragma unroll 2
+      for (int j0 = 0; j0 < cnt; j0 += 2) {
+        const int j = min(j0 + sub, cnt - 1);
+        Halves<V> x = load_head<D, BF16>(p.src, (int64_t)(row + j) * p.stride + (int64_t)h * D, l);
+        norm_rope<D>(x, g, gain != nullptr, p.eps, &tab[j][l * V]);
+        if (j0 + sub < cnt) store_bf16<D>(dst + j * step, x, l);
       }
     }
   }
@@ -321,7 +340,7 @@ cudaError_t launch_qkv_t(const QkvParams& p, bool pdl, cudaStream_t st) {
   const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
   const int warps = kQkvThreads / 32;
   // The heads are split over CTAs until every SM has eight (of rows of 8: sixteen): one head a warp hides the look-ups and the
-  // angles best (append of 3.7 k tokens: 43 us, against 58 with four a SM and 77 with two).
+  // angles best (append of 3.7 k tokens with read-back: 36.4 us, against 44.8 with five a SM; rotation 23.1 against 24.3 with ten).
   int split = ((APPEND ? 8 : 16) * device_sm_count() + windows - 1) / windows;
   if (split > (tasks + warps - 1) / warps) split = (tasks + warps - 1) / warps;
   // the fewest CTAs with as many rounds of heads
