@@ -47,9 +47,10 @@ constexpr int kBlocks = kChunk / TERN_KV_BLOCK;
 constexpr uint32_t kMaxPolls = 1u << 26;          // seconds, then a wait for a stage gives up
 // What a tile costs beside its chunks (queries in, warps joined, result out), in chunks: measured 2.5 us of a
 // CTA that streams a chunk in 0.7 us; with 32 rows and one CTA on the SM 6 to 8 us, of which the last CTA of a tile spends 4
-// on joining the partial results (16 ragged sequences of 8 rows: 71.4 us with a cost of 4, 65.4 with 8, 65.7 with 10).
+// on joining the partial results (16 ragged sequences of 8 rows: 71.4 us with a cost of 4, 65.4 with 8, 65.7 with 10). With 16 rows 4 takes 1 to 2% longer
+// than 7 (16 sequences of 4 rows 70.5 against 69.2 us), with 8 rows 6 does than 4 (64 ragged tokens 77.6 against 76.8).
 template <int R>
-constexpr int kTileCost = R == 32 ? 8 : 4;
+constexpr int kTileCost = R == 32 ? 8 : R == 16 ? 7 : 4;
 
 template <int D, int R>
 struct Shape {
