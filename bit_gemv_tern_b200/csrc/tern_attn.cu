@@ -588,7 +588,12 @@ cudaError_t launch_stream_t(AttnMaps& a, bool pdl, cudaStream_t st) {
 template <int D>
 cudaError_t launch_stream_d(AttnMaps& a, bool pdl, cudaStream_t st) {
   const long long rows = (long long)a.p.max_rows * a.p.group.d;        // of a sequence and head, if the caller is right
-  if (rows > 32) return launch_attn_tile(a, D, pdl, st);
+  // 33 to 64 rows are two tiles here, the cache read twice, and one of the tile kernel. Where the tiles are few beside the SMs both
+  // wait on latency and the stream's is the shorter (one sequence of 16 rows, 16 tiles, over 100 / 1000 / 4000 / 30000 tokens:
+  // 8.8 / 18.9 / 20.3 / 54.6 us against 11.2 / 20.5 / 27.8 / 71.1), with more the tile kernel's (4 sequences, 64 tiles, over 2000:
+  // 27.4 against 24.3; 16 over 4096: 105 against 77).
+  const long long tiles = ((long long)a.p.kv.rows * a.p.group.d + 31) / 32 * a.p.kv.kv_heads;
+  if (rows > 64 || (rows > 32 && tiles * 8 > persistent_grid(kMaxGridCTAs))) return launch_attn_tile(a, D, pdl, st);
   if (rows <= 8) return launch_stream_t<D, 8>(a, pdl, st);
   if (rows <= 16) return launch_stream_t<D, 16>(a, pdl, st);
   return launch_stream_t<D, 32>(a, pdl, st);

@@ -262,6 +262,13 @@ def test_attention_of_many_rows(heads, page, lens):
     run_attn(Paged(51, heads, page, lens, extra_rows=2), 52)
 
 
+@pytest.mark.parametrize("batch", [1, 2, 5])
+@pytest.mark.parametrize("heads,n", [(H8B, 9), (H8B, 16), ((12, 4, 64), 21), ((8, 1, 128), 5)])
+def test_attention_of_33_to_64_rows_of_a_tile(heads, n, batch):
+    P = Paged(69, heads, 32, [(n, 20), (n - 1, 700), (n, n), (0, 9), (n, 3000)][-batch:])
+    run_attn(P, 70, max_rows=n)
+
+
 @pytest.mark.parametrize("max_rows", [1, 4, 16, 10_000])
 def test_attention_is_right_whatever_max_rows_says(max_rows):
     run_attn(Paged(61, H06B, 16, [(1, 90), (70, 200), (5, 5), (0, 0), (1, 0)], extra_rows=1), 62, max_rows)
