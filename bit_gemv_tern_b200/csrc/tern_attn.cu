@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
           *reinterpret_cast<volatile int*>(&sstage[s]) = q;
         }
         if (lane / kBlocks == at)                // ks, log2 vs, 1 / vs of the chunk's blocks
-          *reinterpret_cast<float4*>(sscale + (s * kBlocks + lane % kBlocks) * 4) = make_float4(cur.ks, __log2f(cur.vs), __fdividef(1.0f, cur.vs), 0.0f);
+          *reinterpret_cast<float4*>(sscale + (s * kBlocks + lane % kBlocks) * 4) = make_float4(cur.ks, __log2f(value_scale(cur.vs)), __fdividef(1.0f, value_scale(cur.vs)), 0.0f);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
         if (++at == kAhead) at = 0;

@@ -47,6 +47,11 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// A value block's scale as the exponents carry it: its logarithm and its reciprocal have to be finite, so that zero (a block of
+// zeros by its scale) and what else lies below the smallest scale of an append counts as that. The tokens keep their weight; their
+// values are then 127 * 2^-60 at most. A negative scale or nan stays and makes the rows that see it nan.
+__device__ __forceinline__ float value_scale(float s) { return s >= 0.0f && s < kKvScaleFloor ? kKvScaleFloor : s; }
+
 // R: rows of a tile, CH: tokens of a chunk, COST: what a tile costs beside its chunks, in chunks.
 
 // The walk over tiles: sequence, key/value head, row tile; chunks of a tile.

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
                 const int64_t blk = (int64_t)head * (p.kv.page_size / TERN_KV_BLOCK) + place / TERN_KV_BLOCK;
                 row = head * p.kv.page_size + place;
                 ks = p.kv.ks[blk];
-                vs = p.kv.vs[blk];
+                vs = value_scale(p.kv.vs[blk]);
               } else if (p.kv.flag) {
                 *p.kv.flag = 1;
               }

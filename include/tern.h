@@ -638,8 +638,10 @@ size_t tern_paged_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_
  *   TERN_ETIMEOUT (tern_device_status) it has to be zero-filled again.
  * Codes and queries are multiplied exactly (the queries as fp16 scaled by a power of two of
  * their row's absmax), sums, maxima and the softmax are fp32, the probabilities times the value
- * block's scale are rounded to fp16 for the second product. |value| below 2^27 keeps that scaling
- * exact. Results do not depend on the run, but on the other sequences of the call through the way
+ * block's scale are rounded to fp16 for the second product. Key scales are finite; value scales lie
+ * between 0 and 2^40 (values below 2^46), and one below 2^-60, zero among them, counts as 2^-60: its
+ * tokens keep their weight, their values are 0 but for 127 * 2^-60. A negative value scale or a nan makes
+ * the rows that see it nan. Results do not depend on the run, but on the other sequences of the call through the way
  * the work is split (within rounding).
  * flags: 0 or TERN_FLAG_PDL (the kernel waits for the preceding one before it reads anything). */
 tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softmax_scale, const tern_kv_cache* cache,

@@ -1,0 +1,54 @@
+"""GPU parity of the attention-side operators where they can go wrong: scales of zero, a long flat tail beside one
+strong token, batches above a block of the plan, far positions, large pages, queries that are not finite, calls
+without rows; each against the plain 64-bit forms of kv_util."""
+import numpy as np
+import pytest
+import torch
+
+import bit_gemv_tern_b200 as tg
+from kv_util import BLOCK, Paged, attention, bf16, check_attention, norm_rope
+from test_gpu_kv import H06B, H8B, check_append, close_bf16, dev, host, rows_of, run_append, run_attn, spec_of, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+# (1 .. 8, 9 .. 16, 17 .. 32 rows of a tile, and the tile kernel)
+FEW_AND_MANY = [([(1, 300), (1, 40)], 1), ([(3, 300), (4, 65)], 4), ([(8, 300), (5, 30)], 8), ([(100, 300), (40, 40)], 100)]
+
+
+@pytest.mark.parametrize("lens,max_rows", FEW_AND_MANY)
+def test_attention_over_blocks_with_a_scale_of_zero(lens, max_rows):
+    """Blocks of zeros by their scale, as another quantiser may leave them, beside ordinary ones: their tokens keep
+    their weight. Every row sees the ordinary block 0, beside whose values 127 * 2^-60 does not count."""
+    P = Paged(121, (8, 2, 128), 32, lens)
+    for b, (_, kv) in enumerate(lens):
+        for t in range(0, kv, BLOCK):
+            at = (P.table[b, t // 32], slice(None), t % 32 // BLOCK)
+            if t // BLOCK % 3 == 1:
+                P.vs[at] = 0.0
+            if t // BLOCK % 4 == 2:
+                P.ks[at] = 0.0
+            if t // BLOCK % 5 == 4:
+                P.vs[at] = 2.0 ** -70                      # counts as 2^-60
+    run_attn(P, 122, max_rows)
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("lens,max_rows", FEW_AND_MANY)
+def test_attention_over_a_cache_of_zeros(lens, max_rows, codes):
+    """A cache filled with zeros (codes too, or scales alone) weighs all tokens alike: the outputs are zero (a code of a
+    block without a scale may stand for up to 127 * 2^-60), the log of the sum is that of the tokens seen."""
+    P = Paged(123, (8, 2, 128), 16, lens)
+    P.ks[:], P.vs[:] = 0.0, 0.0
+    if codes:
+        P.k[:], P.v[:] = 0, 0
+    cache, batch = P.device(tg)
+    q = torch.randn(P.rows, 8, 128, device="cuda").to(torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0), torch.full((P.rows, 8), 7.0, device="cuda")
+    tg.tern_paged_attn(q, 0.1, cache, batch, out, workspace((8, 2, 128)), max_rows, lse)
+    assert (np.abs(host(out)) <= (0.0 if codes else 127 * 2.0 ** -60 * (1 + 2.0 ** -8))).all()
+    seen = np.concatenate([kv - n + 1 + np.arange(n) for n, kv in lens])[:, None]
+    # The sum of equal terms in fp32 (2^-24 of it each); it holds the terms times 2^60, so that its logarithm of base 2
+    # is below 60 + log2(300) < 69 and off by an ulp there, 2^-17; the largest exponent, of a size below 61, is off by
+    # half of one, 2^-19. Their sum is exact to 2^-24 of it, and ln 2 * (2^-17 + 2^-19) < 2^-17.
+    assert (np.abs(host(lse) - np.log(seen)) <= 2.0 ** -17 + 2.0 ** -22 * np.log(seen) + 2.0 ** -24 * seen).all()
