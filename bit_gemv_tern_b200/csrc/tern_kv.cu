@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kQkvThreads, APPEND ? 4 : 5) k_qkv(const __gri
     for (int t = threadIdx.x; t < cnt * (D / 2); t += kQkvThreads) {
       const int j = t / (D / 2), e = t % (D / 2);
       const double pos = APPEND ? (double)(pos0 + j) : (double)p.pos[row + j];
-      double turn = pos * (__ldg(p.freq + e) * 0.15915494309189533577);
+      double turn = pos * (p.freq[e] * 0.15915494309189533577);
       turn -= rint(turn);
       float s, c;
       __sincosf(6.283185307179586f * (float)turn, &s, &c);

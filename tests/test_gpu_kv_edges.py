@@ -52,3 +52,36 @@ def test_attention_over_a_cache_of_zeros(lens, max_rows, codes):
     # is below 60 + log2(300) < 69 and off by an ulp there, 2^-17; the largest exponent, of a size below 61, is off by
     # half of one, 2^-19. Their sum is exact to 2^-24 of it, and ln 2 * (2^-17 + 2^-19) < 2^-17.
     assert (np.abs(host(lse) - np.log(seen)) <= 2.0 ** -17 + 2.0 ** -22 * np.log(seen) + 2.0 ** -24 * seen).all()
+
+
+def test_captured_rotations_follow_frequencies_written_just_before():
+    """The frequencies rewritten by the kernel in front of a rotation and of an append with programmatic dependent launch."""
+    heads, rows = H06B, 40
+    spec, g = spec_of(heads, 131)
+    src, x = rows_of(rows, heads, 132, torch.float32)
+    P = Paged(133, heads, 16, [(rows, 100)])
+    cache, batch = P.device(tg)
+    pos = np.arange(60, 100, dtype=np.int32)
+    pos_dev, new = dev(pos), spec.freq.clone()
+    q, qa = (torch.zeros(rows, heads[0], 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k = torch.zeros(rows, heads[1], 128, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        spec.freq.copy_(new)
+        tg.tern_qk_norm_rope(spec, src, pos_dev, q, k, flags=tg.TERN_FLAG_PDL)
+        spec.freq.mul_(2.0)
+        tg.tern_kv_append(spec, src, cache, batch, qa, flags=tg.TERN_FLAG_PDL)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for base in (1e4, 1e6, 5e2):
+        new.copy_(tg.tern_rope_freqs(128, base))
+        graph.replay()
+        torch.cuda.synchronize()
+        f = host(new)
+        close_bf16(host(q), *norm_rope(x[:, :heads[0]], g[0], pos, f, spec.eps))
+        close_bf16(host(k), *norm_rope(x[:, heads[0]:heads[0] + heads[1]], g[1], pos, f, spec.eps))
+        close_bf16(host(qa), *norm_rope(x[:, :heads[0]], g[0], pos, 2 * f, spec.eps))
