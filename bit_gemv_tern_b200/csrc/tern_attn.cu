@@ -24,8 +24,8 @@
 //           1024 + byte). tcgen05 would need M = 128 rows or tokens as the wide operand; at these row
 //           counts the tensor pipe is mostly idle and the bytes bind.
 //   Scales. The exponent of a probability carries the value block's scale, e = log2(e) s + log2(s_v):
-//           p' = 2^(e - max e) is the fp16 operand of the second product and never above 2^8,
-//           whatever the scales; the softmax's sum is sum p' / s_v in fp32.
+//           p' = 2^(e - m), with m up to 2^7 below the largest e, is the fp16 operand of the second product and
+//           never above 2^15, whatever the scales; the softmax's sum is sum p' / s_v in fp32.
 #include <cstdint>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
             if (t0 + g + 8 > p0) c[n][2] = -INFINITY;
             if (t0 + g + 8 > p1) c[n][3] = -INFINITY;
           }
-          rise |= fmaxf(c[n][0], c[n][2]) > m[n][0] + kSlack || fmaxf(c[n][1], c[n][3]) > m[n][1] + kSlack;
+          rise |= fmaxf(c[n][0], c[n][2]) > m[n][0] + (kLift + kSlack) || fmaxf(c[n][1], c[n][3]) > m[n][1] + (kLift + kSlack);
         }
-        // only where some row's maximum rises by more than the slack are the lanes' maxima joined and the sums rescaled
+        // only where some row's maximum rises above the slack are the lanes' maxima joined and the sums rescaled
         if (__any_sync(0xFFFFFFFFu, rise)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(Shape<D, R>::kThreads, Shape<D, R>::kPerSM) k_
               x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, d));
               x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, d));
             }
-            x0 = fmaxf(m[n][0], x0);
-            x1 = fmaxf(m[n][1], x1);
+            x0 = fmaxf(m[n][0], x0 - kLift);
+            x1 = fmaxf(m[n][1], x1 - kLift);
             const float r0 = exp2_approx(m[n][0] - x0), r1 = exp2_approx(m[n][1] - x1);
             m[n][0] = x0;
             m[n][1] = x1;

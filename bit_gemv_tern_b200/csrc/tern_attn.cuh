@@ -17,10 +17,14 @@ namespace tern {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCounterBytes = 8192;               // the workspace's counters, before the partial results
-// The running maximum follows only when it rises by more than this (a power of two of slack in p'
-// instead of a rescale of the output for every small rise).
-constexpr float kSlack = 8.0f;
-// The maximum of no token at all: finite, so that differences of it with itself and with minus infinity are not nan.
+// A row's probabilities p' = 2^(e - m) are rounded to fp16 for the second product while their sum stays in fp32. A term too small
+// for fp16 is then missing from the output but not from the sum, and a long flat tail beside one strong token is made of such terms.
+// So the reference m is set kLift below the row's largest exponent, and follows once that has risen kSlack further (no rescale of the
+// output for every small rise): the largest p' lies between 2^7 and 2^15 (fp16 ends at 65504), and a rounding takes 2^-25 at
+// most, 2^-32 of the largest. With m at the largest exponent itself it took 2^-25 of it: 3000 tokens of 2^-26.5 each were lost.
+// m is common to a row's sum and output, so nothing else depends on it.
+constexpr float kLift = 7.0f, kSlack = 8.0f;
+// The reference of no token at all: finite, so that differences of it with itself and with minus infinity are not nan.
 constexpr float kNoMax = -1e30f;
 
 

@@ -604,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_tile(const __grid_constant
           asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[i & 3]) : "f"(mx[i & 3]), "f"(x), "f"(y));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-          const float nm = fmaxf(m, top), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
+        if (__any_sync(0xFFFFFFFFu, top > m + (kLift + kSlack))) {
+          const float nm = fmaxf(m, top - kLift), f = nm == -INFINITY ? 1.0f : exp2_approx(m - nm);
           m = nm;
           l *= f;
           if (c > 0) {                                               // the products so far are complete: the scores waited for them

@@ -638,7 +638,8 @@ size_t tern_paged_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_
  *   TERN_ETIMEOUT (tern_device_status) it has to be zero-filled again.
  * Codes and queries are multiplied exactly (the queries as fp16 scaled by a power of two of
  * their row's absmax), sums, maxima and the softmax are fp32, the probabilities times the value
- * block's scale are rounded to fp16 for the second product. Key scales are finite; value scales lie
+ * block's scale are rounded to fp16 for the second product (2^-11 of a term, and at least 2^-32 of the
+ * row's largest one: smaller terms add to the sum and not to the output). Key scales are finite; value scales lie
  * between 0 and 2^40 (values below 2^46), and one below 2^-60, zero among them, counts as 2^-60: its
  * tokens keep their weight, their values are 0 but for 127 * 2^-60. A negative value scale or a nan makes
  * the rows that see it nan. Results do not depend on the run, but on the other sequences of the call through the way

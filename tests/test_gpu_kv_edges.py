@@ -85,3 +85,36 @@ def test_captured_rotations_follow_frequencies_written_just_before():
         close_bf16(host(q), *norm_rope(x[:, :heads[0]], g[0], pos, f, spec.eps))
         close_bf16(host(k), *norm_rope(x[:, heads[0]:heads[0] + heads[1]], g[1], pos, f, spec.eps))
         close_bf16(host(qa), *norm_rope(x[:, :heads[0]], g[0], pos, 2 * f, spec.eps))
+
+
+@pytest.mark.parametrize("heads,lens", [
+    (H8B, [(1, 3000)] * 64),
+    (H8B, [(4, 3000)] * 32),
+    (H8B, [(8, 3000)] * 16),
+    (H06B, [(100, 3000), (64, 1500)]),
+])
+def test_attention_keeps_a_long_flat_tail_beside_one_strong_token(heads, lens):
+    """The first token holds nearly all of the probability and a value of zero, every other one 2^-26.5 of its share: the
+    output is the tail's sum. The second product takes a probability times its block's scale in fp16, the largest of a
+    row at 2^7 or above, so that one below 2^-24 there, 2^-31 of the largest, is off by 2^-25 there at most, 2^-32
+    of the largest; fp32 sums over the tokens and the other terms as in kv_util.check_attention."""
+    P = Paged(141, heads, 64, lens)
+    P.k[:], P.vs[:] = 0, 0.02
+    P.v[:] = np.abs(P.v.astype(np.int16)).clip(1, 127).astype(np.int8)
+    for b in range(len(lens)):
+        page = P.table[b, 0]
+        P.k[page, :, 0, 0], P.v[page, :, 0], P.ks[page, :, 0] = 127, 0, 0.01
+    q = np.random.default_rng(142).standard_normal((P.rows, heads[0], heads[2]))
+    q[:, :, 0] = 13.0
+    q = bf16(q)
+    scale = 26.5 * np.log(2.0) / (13.0 * 127 * np.float32(0.01))
+    cache, batch = P.device(tg)
+    out = torch.zeros(P.rows, heads[0], heads[2], dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(P.rows, heads[0], device="cuda")
+    tg.tern_paged_attn(torch.from_numpy(q).to(torch.bfloat16).cuda(), scale, cache, batch, out, workspace(heads), max(n for n, _ in lens), lse)
+    ref, rl, mag, size, small = attention(P, q, np.float64(np.float32(scale)))
+    got, ds = host(out).astype(np.float64), 2.0 ** -20 * size[..., None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -14 + 2 * ds) * mag * (1 + 2.0 ** -8) + 2.0 ** -32 * small
+    assert (tol[:, :, 0].min(1) < 0.2 * ref[:, :, 0].min(1)).all()           # the tail is well above what may be lost
+    assert (np.abs(got - ref) <= tol).all(), np.max(np.abs(got - ref) / tol)
+    assert (np.abs(host(lse) - rl) <= ds[..., 0] + 2.0 ** -20 * (1 + np.abs(rl)) + 2.0 ** -24 * 3000).all()
