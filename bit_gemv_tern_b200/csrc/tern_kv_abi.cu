@@ -19,15 +19,18 @@ bool valid_heads(int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
 }
 constexpr int32_t kMaxRows = 1 << 24;
 
-tern_status check_qkv(const tern_qkv* x, int heads_per_kv) {
-  if (!x || !x->src_dev || !x->freq_dev) return TERN_EINVAL;
+// A call without rows takes null for the tensors of its rows: one of no elements has no address.
+inline bool row_ptr(const void* p, int32_t rows, uintptr_t a) { return (p || rows == 0) && aligned(p, a); }
+
+tern_status check_qkv(const tern_qkv* x, int32_t rows, int heads_per_kv) {
+  if (!x || !x->freq_dev) return TERN_EINVAL;
   if (x->src_type != TERN_ELEM_F32 && x->src_type != TERN_ELEM_BF16) return TERN_EINVAL;
   if (!valid_heads(x->q_heads, x->kv_heads, x->head_dim)) return TERN_ESHAPE;
   if (x->row_stride < (int64_t)(x->q_heads + heads_per_kv * x->kv_heads) * x->head_dim || x->row_stride % 4 ||
       x->row_stride > (int64_t)1 << 32)
     return TERN_ESHAPE;
   if (!(x->eps >= 0.0f) || !std::isfinite(x->eps)) return TERN_EINVAL;
-  if (!aligned(x->src_dev, 16) || !aligned(x->freq_dev, 8) || !aligned(x->q_gain_dev, 4) || !aligned(x->k_gain_dev, 4))
+  if (!row_ptr(x->src_dev, rows, 16) || !aligned(x->freq_dev, 8) || !aligned(x->q_gain_dev, 4) || !aligned(x->k_gain_dev, 4))
     return TERN_EINVAL;
   return TERN_OK;
 }
@@ -70,11 +73,11 @@ extern "C" {
 
 tern_status tern_qk_norm_rope(const tern_qkv* x, int32_t rows, const int32_t* pos_dev, uint16_t* q_dev, uint16_t* k_dev,
                               uint32_t flags, tern_stream_t stream) {
-  tern_status st = check_qkv(x, 1);
+  tern_status st = check_qkv(x, rows, 1);
   if (st != TERN_OK) return st;
-  if (!pos_dev || !q_dev || !k_dev || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
   if (rows < 0 || rows > kMaxRows) return TERN_ESHAPE;
-  if (!aligned(pos_dev, 4) || !aligned(q_dev, 16) || !aligned(k_dev, 16)) return TERN_EINVAL;
+  if (!row_ptr(pos_dev, rows, 4) || !row_ptr(q_dev, rows, 16) || !row_ptr(k_dev, rows, 16) || (flags & ~TERN_FLAG_PDL))
+    return TERN_EINVAL;
   if (rows == 0) return TERN_OK;
   tern::QkvParams p = qkv_params(x, rows, q_dev);
   p.pos = pos_dev;
@@ -84,12 +87,13 @@ tern_status tern_qk_norm_rope(const tern_qkv* x, int32_t rows, const int32_t* po
 
 tern_status tern_kv_append(const tern_qkv* x, const tern_kv_cache* cache, const tern_kv_batch* batch, uint16_t* q_dev,
                            int32_t* err_flag_dev, uint32_t flags, tern_stream_t stream) {
-  tern_status st = check_qkv(x, 2);
+  if (!batch) return TERN_EINVAL;
+  tern_status st = check_qkv(x, batch->rows, 2);
   if (st != TERN_OK) return st;
   tern::KvView v;
   st = check_kv(cache, batch, err_flag_dev, v);
   if (st != TERN_OK) return st;
-  if (!q_dev || !aligned(q_dev, 16) || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
+  if (!row_ptr(q_dev, batch->rows, 16) || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
   if (x->kv_heads != cache->kv_heads || x->head_dim != cache->head_dim) return TERN_ESHAPE;
   if (batch->rows == 0) return TERN_OK;
   tern::QkvParams p = qkv_params(x, batch->rows, q_dev);
@@ -102,7 +106,7 @@ tern_status tern_kv_read(const tern_kv_cache* cache, const tern_kv_batch* batch,
   tern::KvReadParams p = {};
   tern_status st = check_kv(cache, batch, err_flag_dev, p.kv);
   if (st != TERN_OK) return st;
-  if (!k_dev || !v_dev || !aligned(k_dev, 16) || !aligned(v_dev, 16)) return TERN_EINVAL;
+  if (!row_ptr(k_dev, batch->rows, 16) || !row_ptr(v_dev, batch->rows, 16)) return TERN_EINVAL;
   if (batch->rows == 0) return TERN_OK;
   p.k = k_dev;
   p.v = v_dev;
@@ -120,10 +124,11 @@ tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softma
   tern::AttnParams p = {};
   tern_status st = check_kv(cache, batch, err_flag_dev, p.kv);
   if (st != TERN_OK) return st;
-  if (!q_dev || !out_dev || !workspace_dev || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
+  if (!workspace_dev || (flags & ~TERN_FLAG_PDL)) return TERN_EINVAL;
   if (!valid_heads(q_heads, cache->kv_heads, cache->head_dim) || max_rows < 1 || (int64_t)batch->rows * q_heads > INT32_MAX - 64)
     return TERN_ESHAPE;
-  if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16)) return TERN_EINVAL;
+  if (!row_ptr(q_dev, batch->rows, 16) || !row_ptr(out_dev, batch->rows, 16) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
+    return TERN_EINVAL;
   if (!std::isfinite(softmax_scale)) return TERN_EINVAL;
   if (workspace_bytes < tern::attn_workspace_bytes(cache->head_dim)) return TERN_EINVAL;
   if (batch->rows == 0) return TERN_OK;

@@ -540,7 +540,8 @@ tern_status fv5b_head_gemv_argmax(const int8_t* W_dev, const float* block_scale_
  * Rows: a call works on `rows` activation rows; sequence b owns rows row_start[b] .. row_start[b + 1)
  * (n_b of them, none is allowed), and its row i is token kv_len[b] - n_b + i: kv_len counts the
  * tokens in the cache with this call's own among them. Rows behind the last sequence belong to
- * nobody: they are not read and their outputs are left as they were.
+ * nobody: they are not read and their outputs are left as they were. A call of no rows at all enqueues
+ * nothing, and its tensors of rows may be null (so may those of tern_qk_norm_rope).
  *
  * row_start, kv_len and page_table live on the device and may change between the replays of a
  * captured call. What only the device can see of them is checked there: a sequence with row_start

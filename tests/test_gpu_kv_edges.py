@@ -118,3 +118,22 @@ def test_attention_keeps_a_long_flat_tail_beside_one_strong_token(heads, lens):
     assert (tol[:, :, 0].min(1) < 0.2 * ref[:, :, 0].min(1)).all()           # the tail is well above what may be lost
     assert (np.abs(got - ref) <= tol).all(), np.max(np.abs(got - ref) / tol)
     assert (np.abs(host(lse) - rl) <= ds[..., 0] + 2.0 ** -20 * (1 + np.abs(rl)) + 2.0 ** -24 * 3000).all()
+
+
+def test_calls_without_rows_leave_everything_alone():
+    """Tensors of zero rows have no address: such calls are fine and launch nothing."""
+    heads = H06B
+    P = Paged(151, heads, 16, [(0, 20), (0, 0)])
+    cache, batch = P.device(tg)
+    spec, _ = spec_of(heads, 152)
+    before = [host(t).copy() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    none = lambda *s, t=torch.bfloat16: torch.zeros(0, *s, dtype=t, device="cuda")  # noqa: E731
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    src, q, k = none(32 * 128, t=torch.float32), none(16, 128), none(8, 128)
+    tg.tern_qk_norm_rope(spec, src, none(t=torch.int32), q, k)
+    tg.tern_kv_append(spec, src, cache, batch, q, flag)
+    tg.tern_kv_read(cache, batch, k, none(8, 128), flag)
+    tg.tern_paged_attn(q, 0.1, cache, batch, none(16, 128), workspace(heads), 1, none(16, t=torch.float32), flag)
+    assert tg.tern_read_flag(flag) == tg.TERN_OK
+    for a, t in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+        assert (a.view(np.uint8) == host(t).view(np.uint8)).all()
