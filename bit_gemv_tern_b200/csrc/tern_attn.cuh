@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
 
 // A value block's scale as the exponents carry it: its logarithm and its reciprocal have to be finite, so that zero (a block of
 // zeros by its scale) and what else lies below the smallest scale of an append counts as that. The tokens keep their weight; their
-// values are then 127 * 2^-60 at most. A negative scale or nan stays and makes the rows that see it nan.
+// values are then 127 * 2^-60 at most. A negative scale or nan stays one and shows as nan.
 __device__ __forceinline__ float value_scale(float s) { return s >= 0.0f && s < kKvScaleFloor ? kKvScaleFloor : s; }
 
 // R: rows of a tile, CH: tokens of a chunk, COST: what a tile costs beside its chunks, in chunks.

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kQkvThreads, APPEND ? 4 : 5) k_qkv(const __gri
       cnt = min(TERN_KV_BLOCK - pos0 % TERN_KV_BLOCK, end - row);
       __syncthreads();                                          // the last unit's table is done with
     }
-    // angles in turns, reduced in fp64 to half a turn; the fast sine and cosine are good to 2^-21 there
+    // angles in turns, reduced in fp64 to half a turn (three roundings: off by 3 * 2^-53 of the unreduced angle at most); the fast
+    // sine and cosine are good to 2^-21 there
     for (int t = threadIdx.x; t < cnt * (D / 2); t += kQkvThreads) {
       const int j = t / (D / 2), e = t % (D / 2);
       const double pos = APPEND ? (double)(pos0 + j) : (double)p.pos[row + j];

@@ -579,8 +579,9 @@ typedef struct {
 /* Rows of a q|k|v output and what turns them into queries and keys: per head vector x,
  *   z = x * r * gain, r = 1 / sqrt(sum x^2 / head_dim + eps)      (gain NULL: z = x, no norm)
  *   y_i = z_i cos a_i - z_(i + D/2) sin a_i,  y_(i + D/2) = z_(i + D/2) cos a_i + z_i sin a_i,
- * a_i = position * freq[i], i < D/2 = head_dim / 2. Norm and rotation are in fp32, the angle is
- * reduced in fp64 (exact to 1e-9 of a turn at every position an int32 holds), and a result is
+ * a_i = position * freq[i], i < D/2 = head_dim / 2. Norm and rotation are in fp32, with a sine and cosine
+ * good to 2^-21. The angle is multiplied and reduced in fp64: off by at most 3 * 2^-53 of itself, which for a
+ * frequency of 1 is 1e-9 of a turn at position 2^24 and 1.2e-7 at 2^31 - 1. A result is
  * rounded once: to bf16 (q, and k outside the cache) or to its int8 code. Values are left alone.
  * Inputs are finite. */
 typedef struct {
@@ -637,13 +638,14 @@ size_t tern_paged_attn_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_
  *   before its first use; every call leaves its counters zero again, so one buffer serves any number of
  *   calls in stream order (two calls, or two captured graphs, that overlap in time need two). After
  *   TERN_ETIMEOUT (tern_device_status) it has to be zero-filled again.
- * Codes and queries are multiplied exactly (the queries as fp16 scaled by a power of two of
- * their row's absmax), sums, maxima and the softmax are fp32, the probabilities times the value
- * block's scale are rounded to fp16 for the second product (2^-11 of a term, and at least 2^-32 of the
- * row's largest one: smaller terms add to the sum and not to the output). Key scales are finite; value scales lie
- * between 0 and 2^40 (values below 2^46), and one below 2^-60, zero among them, counts as 2^-60: its
- * tokens keep their weight, their values are 0 but for 127 * 2^-60. A negative value scale or a nan makes
- * the rows that see it nan. Results do not depend on the run, but on the other sequences of the call through the way
+ * Queries are finite. They are multiplied by the codes as fp16, scaled by a power of two of their row's absmax: elements
+ * from 2^-30 of it on exactly, smaller ones to 2^-38 of it. Sums, maxima and the softmax are fp32, with a fast exponential
+ * (2^-22). For the second product a probability times its value block's scale is rounded to fp16: to 2^-11 of itself or
+ * 2^-32 of the row's largest, whichever is more (what that drops still counts in the sum).
+ * Key scales are finite. Value scales lie between 0 and 2^40 (values below 2^46); one below 2^-60, zero
+ * among them, counts as 2^-60, so that its tokens keep their weight and add less than 2^-53 to an element. Other value
+ * scales are the caller's error and give nan or a wrong weight in the rows of their sequence.
+ * Results do not depend on the run, but on the other sequences of the call through the way
  * the work is split (within rounding).
  * flags: 0 or TERN_FLAG_PDL (the kernel waits for the preceding one before it reads anything). */
 tern_status tern_paged_attn(const uint16_t* q_dev, int32_t q_heads, float softmax_scale, const tern_kv_cache* cache,

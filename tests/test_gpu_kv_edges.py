@@ -137,3 +137,59 @@ def test_calls_without_rows_leave_everything_alone():
     assert tg.tern_read_flag(flag) == tg.TERN_OK
     for a, t in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
         assert (a.view(np.uint8) == host(t).view(np.uint8)).all()
+
+
+def far_rope(x, gain, pos, freq):
+    """norm_rope of kv_util with the angles in extended precision."""
+    D = x.shape[-1]
+    z = x / np.sqrt((x ** 2).mean(-1, keepdims=True) + 1e-6) * gain
+    a = np.asarray(pos, np.longdouble)[:, None] * np.asarray(freq, np.longdouble)
+    a = a - np.rint(a / (2 * np.longdouble(np.pi))) * (2 * np.longdouble("3.14159265358979323846264338327950288"))
+    c, s = np.cos(a).astype(np.float64)[:, None], np.sin(a).astype(np.float64)[:, None]
+    lo, hi = z[..., :D // 2], z[..., D // 2:]
+    return np.concatenate([lo * c - hi * s, hi * c + lo * s], -1), np.tile(np.abs(lo) + np.abs(hi), 2)
+
+
+def test_qk_norm_rope_at_the_last_positions():
+    """Up to 2^31 - 1: the angle is a product in fp64 of at most 2^31 / (2 pi) turns, off by 6.2e-8 of a turn (3 * 2^-53
+    of it at most, 2^-20 in radians), within close_bf16's 2^-18 together with the sine's 2^-21."""
+    heads, rows = H8B, 130
+    spec, g = spec_of(heads, 161)
+    src, x = rows_of(rows, heads, 162, torch.float32)
+    pos = np.concatenate([2 ** 31 - 1 - np.arange(65), np.random.default_rng(163).integers(2 ** 30, 2 ** 31, 65)]).astype(np.int32)
+    q = torch.zeros(rows, heads[0], 128, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(rows, heads[1], 128, dtype=torch.bfloat16, device="cuda")
+    tg.tern_qk_norm_rope(spec, src, dev(pos), q, k)
+    f = host(spec.freq)
+    close_bf16(host(q), *far_rope(x[:, :heads[0]], g[0], pos, f))
+    close_bf16(host(k), *far_rope(x[:, heads[0]:heads[0] + heads[1]], g[1], pos, f))
+
+
+def test_append_and_read_at_the_end_of_the_longest_table():
+    """Rows whose tokens are the last of 32766 pages of 65536, all the same page of memory but the last two."""
+    heads, page, pages = (2, 1, 64), 65536, 32766
+    spec, g = spec_of(heads, 165)
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    table[0, -2], table[0, -1] = 2, 1
+    kv, n = (pages - 1) * page + 20, 50                # 30 tokens in the last but one page, 20 in the last
+    codes = [torch.zeros(3, 1, page, 64, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(3, 1, page // BLOCK, device="cuda") for _ in range(2)]
+    cache = tg.KvCache(*codes, *scales)
+    batch = tg.KvBatch(dev(np.array([0, n], np.int32)), dev(np.array([kv], np.int32)), table, n)
+    src, x = rows_of(n, heads, 166, torch.float32)
+    q = torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tg.tern_kv_append(spec, src, cache, batch, q, flag)
+    tg.tern_kv_read(cache, batch, k, v, flag)
+    assert tg.tern_read_flag(flag) == tg.TERN_OK
+    f, pos = host(spec.freq), np.arange(kv - n, kv)
+    close_bf16(host(q), *far_rope(x[:, :2], g[0], pos, f))
+    want, size = far_rope(x[:, 2:3], g[1], pos, f)
+    for got, y, sz in ((host(k), want, size), (host(v), x[:, 3:], 0 * size)):
+        # half a step of the block's 127 (the largest of its appended rows: none came before), then bf16
+        blocks = pos // BLOCK
+        top = np.array([np.abs(y[blocks == b]).max() for b in blocks])[:, None, None]
+        assert (np.abs(got - y) <= top / 127 * (0.5 + 2.0 ** -9) + 2.0 ** -8 * np.abs(y) + 2.0 ** -17 * (sz + top)).all()
+    assert not codes[0][0].any() and not codes[1][0].any()
+    assert codes[0][2, 0, -30:].any(1).all() and codes[0][1, 0, :20].any(1).all() and not codes[0][1, 0, 20:].any()
