@@ -193,3 +193,79 @@ def test_append_and_read_at_the_end_of_the_longest_table():
         assert (np.abs(got - y) <= top / 127 * (0.5 + 2.0 ** -9) + 2.0 ** -8 * np.abs(y) + 2.0 ** -17 * (sz + top)).all()
     assert not codes[0][0].any() and not codes[1][0].any()
     assert codes[0][2, 0, -30:].any(1).all() and codes[0][1, 0, :20].any(1).all() and not codes[0][1, 0, 20:].any()
+
+
+@pytest.mark.parametrize("lens,max_rows", [([(1, 20_000)] * 2, 1), ([(4, 9000)] * 3, 4), ([(8, 9000)] * 3, 8), ([(200, 6000), (130, 900)], 200)])
+def test_attention_leaves_every_counter_of_its_workspace_zero(lens, max_rows):
+    """Tiles that many CTAs share: their counters (the workspace's first 8192 bytes) serve the next call."""
+    _, _, _, ws = run_attn(Paged(171, H8B, 64, lens), 172, max_rows)
+    assert not ws[:8192].any()
+    assert ws[8192:].any()                              # there were partial results
+
+
+def many(count, n_most, empty, seed):
+    """Lengths of many short sequences, among them some without rows, without tokens, and (`empty`) rows that see nothing."""
+    r = np.random.default_rng(seed)
+    lens = []
+    for b in range(count):
+        n = int(r.integers(0, n_most + 1))
+        kv = int(r.integers(0, 40)) + (0 if empty else n)
+        lens.append((n, 0 if empty and b % 17 == 3 else kv))
+    lens[-1] = (n_most, n_most + 33)
+    return lens
+
+
+@pytest.mark.parametrize("count", [192, 193, 256, 257, 512, 513, 1200])
+@pytest.mark.parametrize("heads,n_most,max_rows", [((4, 2, 64), 1, 1), ((8, 2, 128), 3, 3), ((8, 2, 128), 6, 6), ((4, 1, 64), 5, 500)])
+def test_attention_of_batches_above_a_block_of_the_plan(count, heads, n_most, max_rows):
+    run_attn(Paged(181, heads, 16, many(count, n_most, True, count), extra_rows=2), 182, max_rows)
+
+
+@pytest.mark.parametrize("count", [256, 257, 700])
+@pytest.mark.parametrize("n_most", [1, 3, 40])
+def test_append_to_batches_above_a_block(count, n_most):
+    heads = (2, 1, 64)
+    P = Paged(183, heads, 32, many(count, n_most, False, count + 1), extra_rows=1)
+    spec, g = spec_of(heads, 184)
+    cache, batch, _ = run_append(P, spec, g, torch.float32, 185)
+    k, v = (torch.full((P.rows, 1, 64), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tg.tern_kv_read(cache, batch, k, v)
+    P.k, P.v, P.ks, P.vs = (host(t) for t in (cache.k, cache.v, cache.k_scale, cache.v_scale))
+    for w, got in (("k", host(k)), ("v", host(v))):
+        for b, (n, kv) in enumerate(P.lens):
+            if n:                                       # an exact product of 8 and 24 bits, to fp32 and to bf16
+                want = P.values(b, w)[kv - n:].astype(np.float32)
+                assert (got[P.row_start[b]:P.row_start[b + 1]] == bf16(want)).all()
+        assert (got[P.row_start[-1]:] == 3.0).all()
+
+
+@pytest.mark.parametrize("page", [192, 256, 1040, 65536])
+def test_large_pages(page):
+    heads = (4, 2, 64)
+    P = Paged(191, heads, page, [(1, 2500), (70, 1300), (6, 6)], spare=0)
+    spec, g = spec_of(heads, 192)
+    run_append(P, spec, g, torch.float32, 193)
+    for max_rows in (1, 8, 500):
+        run_attn(Paged(194, heads, page, [(1, 2500), (70, 1300), (6, 6)], spare=0), 195, max_rows)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,max_rows", [([(1, 300), (1, 40)], 1), ([(3, 300), (4, 65)], 4), ([(8, 300), (5, 30)], 8), ([(100, 300), (40, 40)], 100)])
+def test_a_query_that_is_not_finite_spoils_its_own_row_and_head_only(lens, max_rows, bad):
+    P = Paged(201, (8, 2, 128), 32, lens)
+    P.k[..., 5][P.k[..., 5] == 0] = 1                   # +-infinity or nan scores, and both signs of infinity in every block
+    P.k[:, :, ::2, 5], P.k[:, :, 1::2, 5] = np.abs(P.k[:, :, ::2, 5].astype(np.int16)).astype(np.int8), -np.abs(P.k[:, :, 1::2, 5].astype(np.int16)).astype(np.int8)
+    cache, batch = P.device(tg)
+    q = torch.from_numpy(bf16(np.random.default_rng(202).standard_normal((P.rows, 8, 128)))).to(torch.bfloat16)
+    row, head = int(P.row_start[1]) - 1, 3
+    dirty = q.clone()
+    dirty[row, head, 5] = bad
+    ws, got = workspace((8, 2, 128)), []
+    for x in (q, dirty):
+        out, lse = torch.full((P.rows, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((P.rows, 8), 7.0, device="cuda")
+        tg.tern_paged_attn(x.cuda(), 0.09, cache, batch, out, ws, max_rows, lse)
+        got.append((host(out), host(lse)))
+    (out, lse), (out2, lse2) = got
+    assert np.isnan(out2[row, head]).all() and np.isnan(lse2[row, head])
+    out2[row, head], lse2[row, head] = out[row, head], lse[row, head]
+    check_attention(P, q.double().numpy(), 0.09, out2, lse2)
