@@ -194,7 +194,7 @@ __device__ __forceinline__ void append_head(const QkvParams& p, bool is_k, int h
   if (lane == 0 && s != old) *scale = s;
 }
 
-// 64 registers a thread where it appends, 51 where not: 36.4 and 23.1 us (append with read-back, 3.7 k tokens; rotation, 4095
+// 64 registers a thread where it appends, 48 where not: 36.4 and 23.1 us (append of 2496 rows with read-back; rotation, 4095
 // rows); with one CTA more on the SM 38.2 and 24.7, with one less 38.2 and 23.8.
 template <int D, bool BF16, bool APPEND, int W>
 __global__ void __launch_bounds__(kQkvThreads, APPEND ? 4 : 5) k_qkv(const __grid_constant__ QkvParams p) {
@@ -341,7 +341,7 @@ cudaError_t launch_qkv_t(const QkvParams& p, bool pdl, cudaStream_t st) {
   const int tasks = p.q_heads + (APPEND ? 2 : 1) * p.kv_heads;
   const int warps = kQkvThreads / 32;
   // The heads are split over CTAs until every SM has eight (of rows of 8: sixteen): one head a warp hides the look-ups and the
-  // angles best (append of 3.7 k tokens with read-back: 36.4 us, against 44.8 with five a SM; rotation 23.1 against 24.3 with ten).
+  // angles best (append of 2496 rows with read-back: 36.4 us, against 44.8 with five a SM; rotation 23.1 against 24.3 with ten).
   int split = ((APPEND ? 8 : 16) * device_sm_count() + windows - 1) / windows;
   if (split > (tasks + warps - 1) / warps) split = (tasks + warps - 1) / warps;
   // the fewest CTAs with as many rounds of heads
